@@ -18,6 +18,7 @@ KKT_ERR_CUDA = 4
 KKT_ERR_SEQLENS = 5
 KKT_ERR_TIMEOUT = 6
 KKT_ERR_NO_DEVICE = 7
+KKT_ERR_INDEX = 8
 
 KKT_IO_BF16 = 0
 KKT_IO_F32 = 1
@@ -33,6 +34,11 @@ KKT_WORKSPACE_BYTES = 256
 KKT_HOST_MAX_PIECES = 64
 KKT_NOALLOC_SCRATCH_BYTES = 256
 
+GDN_OUT_BF16 = 0
+GDN_OUT_F32 = 1
+GDN_OUT_E4M3 = 2
+GDN_COPY_MAX_TENSORS = 64
+
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
@@ -45,6 +51,11 @@ SIGNATURES = {
     "kkt_solve_fwd_noalloc": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
     "gdn_chunk_state_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, ctypes.c_float, _vp,
                                  _vp, _vp]),
+    "gdn_recurrent_fwd": (_i, [_vp] * 6 + [_i] * 6 + [ctypes.c_float, _i, _vp, _i, _i, _vp, _vp, _vp, _vp]),
+    "gdn_prep_fwd": (_i, [_vp] * 8 + [_i] * 7 + [ctypes.c_float, _i, _i, _vp, _i] + [_vp] * 7),
+    "add_rms_norm_fwd": (_i, [_vp, _vp, _vp, _sz, _i, ctypes.c_float, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "gated_rms_norm_fwd": (_i, [_vp, _vp, _vp, _sz, _i, ctypes.c_float, _i, _i, _vp, _vp, _vp]),
+    "gdn_state_copy": (_i, [_vp] * 5 + [_i, _vp, _vp, _i, _i, _i, _vp]),
     "kkt_host_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i, _i]),
     "kkt_solve_fwd_host": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _sz,
                                 _vp]),

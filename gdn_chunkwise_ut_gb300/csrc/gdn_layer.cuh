@@ -1,0 +1,189 @@
+// gdn_layer.cuh -- what the serving operators (include/gdn_layer.h) share: vector loads and stores
+// converted to and from fp32, the sequence bounds, and the launch with programmatic stream
+// serialisation.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gdn_layer.h"
+#include "kkt_internal.cuh"
+#include "sm100_ptx.cuh"
+
+namespace kkt {
+
+inline bool aligned_ptr(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Four consecutive values as fp32 (the address a multiple of 4 values).
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    uint2 w;
+    w.x = *reinterpret_cast<const uint32_t *>(&a);
+    w.y = *reinterpret_cast<const uint32_t *>(&b);
+    *reinterpret_cast<uint2 *>(p) = w;
+}
+
+// Eight consecutive values, raw and as fp32 (the address a multiple of 8 values).
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+    float4 a, b;
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 a;
+};
+__device__ __forceinline__ Raw8<float> raw8(const float *p) {
+    return {*reinterpret_cast<const float4 *>(p), *reinterpret_cast<const float4 *>(p + 4)};
+}
+__device__ __forceinline__ Raw8<__nv_bfloat16> raw8(const __nv_bfloat16 *p) {
+    return {*reinterpret_cast<const uint4 *>(p)};
+}
+__device__ __forceinline__ void widen8(const Raw8<float> &r, float (&v)[8]) {
+    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+    v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+}
+__device__ __forceinline__ void widen8(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// In 8 bits; values past the type's largest are held at it (a NaN stays one).
+__device__ __forceinline__ void store8(__nv_fp8_e4m3 *p, const float (&v)[8]) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | (hi << 16);
+    }
+    *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __nv_fp8_e4m3 from_f32<__nv_fp8_e4m3>(float x) {
+    __nv_fp8_e4m3 y;
+    y.__x = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+    return y;
+}
+
+// x / (1 + e^-x) by the hardware's exponential and reciprocal: a few parts in 10^7.
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+
+// Sum (maximum) over aligned groups of W lanes.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+template <int W>
+__device__ __forceinline__ float lanes_max(float x) {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// The scale that takes a group's largest magnitude to the 8-bit type's largest value.  A group of
+// zeros has 1; below 2^-126 the scale stays a normal number, so that its reciprocal is finite.
+__device__ __forceinline__ float e4m3_scale(float top) {
+    return top > 0.f ? fmaxf(__fdiv_rn(top, 448.f), 1.17549435e-38f) : 1.f;
+}
+
+// Tokens [a, b) of sequence n; ok is false (and the error recorded) where cu_seqlens is malformed.
+struct Span {
+    int64_t a, b;
+    bool ok;
+};
+__device__ __forceinline__ Span seq_span(const int32_t *cu, int n, int N, int T, int64_t ntok, int *status) {
+    Span s;
+    s.a = seq_start(cu, n, T);
+    s.b = seq_start(cu, n + 1, T);
+    s.ok = s.a >= 0 && s.b >= s.a && s.b <= ntok && (n > 0 || s.a == 0) && (n < N - 1 || s.b == ntok);
+    if (!s.ok) record_error(status, KKT_ERR_SEQLENS);
+    return s;
+}
+
+// The slot of sequence n: negative: none; ok is false (and the error recorded) past the pool's end.
+__device__ __forceinline__ int slot_of(const int32_t *slots, int n, int num_slots, int *status, bool &ok) {
+    const int s = slots ? __ldg(slots + n) : n;
+    if (s >= num_slots) {
+        record_error(status, KKT_ERR_INDEX);
+        ok = false;
+    }
+    return s;
+}
+
+// SMs of the current device (looked up once per device).
+inline int sm_count_cached() {
+    static std::atomic<int> known[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// Launch whose blocks may be scheduled while the previous kernel on the stream finishes; the kernel
+// waits (griddep_wait) before it touches global memory.
+template <typename... Params, typename... Args>
+inline int launch_serialised(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, Params(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return KKT_ERR_CUDA;
+    }
+    return KKT_OK;
+}
+
+}  // namespace kkt

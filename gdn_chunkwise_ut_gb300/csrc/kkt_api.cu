@@ -171,6 +171,7 @@ extern "C" const char *kkt_status_string(int status) {
         case KKT_ERR_SEQLENS: return "malformed cu_seqlens";
         case KKT_ERR_TIMEOUT: return "device-side wait timed out";
         case KKT_ERR_NO_DEVICE: return "no usable CUDA device";
+        case KKT_ERR_INDEX: return "slot index out of range";
         default: return "unknown status";
     }
 }

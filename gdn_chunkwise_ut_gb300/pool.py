@@ -1,0 +1,125 @@
+"""Slots for the states of a server's sequences.
+
+``SlotTable`` is the bookkeeping (which slots are live), plain Python; ``StatePool`` adds the tensors of
+a model's layers, the delta rule's states and the short convolutions', and moves slots between them on
+the GPU with ``gdn_state_copy``: every layer's pools in one launch.
+"""
+from __future__ import annotations
+
+import heapq
+
+import torch
+
+from . import _lib
+from .layer import gdn_state_copy
+
+
+class SlotTable:
+    """Which of ``num_slots`` slots are live.  The lowest free slots are handed out first."""
+
+    def __init__(self, num_slots: int):
+        if num_slots < 1:
+            raise ValueError("num_slots must be positive")
+        self.num_slots = int(num_slots)
+        self._free = list(range(self.num_slots))  # a heap
+        self._live = set()
+
+    def __len__(self) -> int:
+        return len(self._live)
+
+    @property
+    def free_slots(self) -> int:
+        return len(self._free)
+
+    def is_live(self, slot: int) -> bool:
+        return slot in self._live
+
+    def alloc(self, n: int = 1) -> list:
+        """``n`` new slots, or none at all (RuntimeError) where fewer are free."""
+        if n < 0:
+            raise ValueError("n must not be negative")
+        if n > len(self._free):
+            raise RuntimeError(f"{n} slots wanted, {len(self._free)} of {self.num_slots} free")
+        slots = [heapq.heappop(self._free) for _ in range(n)]
+        self._live.update(slots)
+        return slots
+
+    def require(self, slots) -> list:
+        slots = [int(s) for s in slots]
+        for s in slots:
+            if s not in self._live:
+                raise ValueError(f"slot {s} is not live")
+        if len(set(slots)) != len(slots):
+            raise ValueError("a slot is named twice")
+        return slots
+
+    def free(self, slots) -> None:
+        slots = self.require(slots)
+        for s in slots:
+            self._live.remove(s)
+            heapq.heappush(self._free, s)
+
+    def compact(self) -> dict:
+        """Moves the live slots into the lowest ones: returns {old: new} for those that move.  The moves
+        are from slots at or past the number of live ones into free slots below it, so that no move
+        writes what another one reads."""
+        n = len(self._live)
+        holes = [s for s in range(n) if s not in self._live]
+        moves = dict(zip(sorted(s for s in self._live if s >= n), holes))
+        self._live = set(range(n))
+        self._free = list(range(n, self.num_slots))
+        return moves
+
+
+class StatePool:
+    """The states of up to ``num_slots`` sequences in every layer of a model.
+
+    ``states[l]`` [num_slots, Hv, dk, dv] (``state_dtype``) and ``convs[l]`` [num_slots, taps - 1, D]
+    (``dtype``, D = 2 Hk dk + Hv dv) are layer l's, as ``gdn_recurrent_fwd`` and ``gdn_prep_fwd`` take
+    them.  The methods run on ``stream`` (default: the current one), which has to be ordered with the
+    calls that use the slots.
+    """
+
+    def __init__(self, num_slots: int, layers: int, Hk: int, Hv: int, dk: int, dv: int, *, taps: int = 4,
+                 state_dtype=torch.float32, dtype=torch.bfloat16, device="cuda"):
+        if 2 * layers > _lib.GDN_COPY_MAX_TENSORS:
+            raise ValueError(f"at most {_lib.GDN_COPY_MAX_TENSORS // 2} layers in one pool")
+        self.table = SlotTable(num_slots)
+        self.states = [torch.zeros((num_slots, Hv, dk, dv), dtype=state_dtype, device=device) for _ in range(layers)]
+        self.convs = [torch.zeros((num_slots, taps - 1, 2 * Hk * dk + Hv * dv), dtype=dtype, device=device)
+                      for _ in range(layers)]
+        self._all = self.states + self.convs
+        self._device = torch.device(device)
+
+    def index(self, slots, *, stream=None) -> torch.Tensor:
+        """The slots as the int32 tensor that the operators take, for use on ``stream``."""
+        with torch.cuda.stream(stream):  # its memory belongs to that stream (None: the current one)
+            return torch.tensor([int(s) for s in slots], dtype=torch.int32, device=self._device)
+
+    def alloc(self, n: int = 1, *, stream=None) -> list:
+        """``n`` slots of zero states."""
+        slots = self.table.alloc(n)
+        if slots:
+            gdn_state_copy(self._all, self.index(slots, stream=stream), stream=stream)
+        return slots
+
+    def fork(self, slot: int, n: int = 1, *, stream=None) -> list:
+        """``n`` new slots, each with a copy of ``slot``'s states."""
+        self.table.require([slot])
+        slots = self.table.alloc(n)
+        if slots:
+            gdn_state_copy(self._all, self.index(slots, stream=stream), self._all,
+                           self.index([slot] * n, stream=stream), stream=stream)
+        return slots
+
+    def free(self, slots) -> None:
+        """Gives the slots back.  Their contents stay until they are handed out again."""
+        self.table.free(slots)
+
+    def compact(self, *, stream=None) -> dict:
+        """Moves the live slots into the lowest ones: returns {old: new} for the slots that moved."""
+        moves = self.table.compact()
+        if moves:
+            gdn_state_copy(self._all, self.index(moves.values(), stream=stream), self._all,
+                           self.index(moves.keys(), stream=stream), stream=stream)
+        return moves

@@ -72,7 +72,8 @@ typedef enum kkt_status {
     KKT_ERR_CUDA = 4,        /* a CUDA runtime / driver call failed */
     KKT_ERR_SEQLENS = 5,     /* device saw a malformed cu_seqlens (kkt_device_status) */
     KKT_ERR_TIMEOUT = 6,     /* a device-side bounded wait expired (kkt_device_status) */
-    KKT_ERR_NO_DEVICE = 7    /* no usable CUDA device / not an sm_103 device */
+    KKT_ERR_NO_DEVICE = 7,   /* no usable CUDA device / not an sm_103 device */
+    KKT_ERR_INDEX = 8        /* device saw a pool slot past the pool's end (gdn_layer.h; kkt_device_status) */
 } kkt_status;
 
 /* I/O dtype of k, v, W_out, U_out (beta is always fp32; T_out is fp32 unless KKT_T_OUT_F16). */
@@ -283,7 +284,7 @@ int kkt_solve_fwd_host(const void *k, const void *v, const float *beta, const fl
 /*
  * kkt_device_status -- synchronises `stream`, then returns and clears the
  * status word of the current device: KKT_OK, or the first device-side error
- * (KKT_ERR_SEQLENS, KKT_ERR_TIMEOUT) recorded since the last call; KKT_ERR_CUDA
+ * (KKT_ERR_SEQLENS, KKT_ERR_TIMEOUT, KKT_ERR_INDEX) recorded since the last call; KKT_ERR_CUDA
  * if the synchronisation itself failed.
  */
 int kkt_device_status(struct CUstream_st *stream);

@@ -1,0 +1,163 @@
+"""add_rms_norm_fwd and gated_rms_norm_fwd against fp64, every output type, at the widths, rows and values
+where they can go wrong (GPU)."""
+import numpy as np
+import pytest
+import torch
+
+from gdn_chunkwise_ut_gb300 import _lib, add_rms_norm_fwd, gated_rms_norm_fwd
+from tests.layer_compare import FP32_VALUE, check_e4m3, check_rounded, norm_ref, silu_ref, to64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+FP8 = torch.float8_e4m3fn
+
+
+def randn(*shape, seed=0, scale=1.0, io=torch.bfloat16):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    return (scale * torch.randn(shape, generator=gen, device=DEV)).to(io)
+
+
+def check_out(y, scales, ref, group):
+    """y (and its scales) against the fp64 norm; group: values to a scale."""
+    if y.dtype != FP8:
+        assert scales is None
+        check_rounded(y, ref, FP32_VALUE, "y")
+        return
+    dim = ref.shape[-1]
+    n = -(-dim // group)
+    pad = np.pad(np.abs(ref), [(0, 0)] * (ref.ndim - 1) + [(0, n * group - dim)])
+    top = pad.reshape(*ref.shape[:-1], n, group).max(-1) / 448
+    top = np.where(top > 0, top, 1.0)
+    s = to64(scales).reshape(top.shape)
+    assert np.all(np.abs(s - top) <= FP32_VALUE * top)
+    check_e4m3(y, np.repeat(s, group, -1)[..., :dim], ref, "y")
+
+
+@pytest.mark.parametrize("dim", [1, 7, 8, 127, 128, 130, 264, 1000, 2048, 2056, 4097, 6144, 8192, 16383, 16384])
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32, FP8])
+def test_add_rms_norm_widths_and_types(dim, io, out):
+    for rows, with_r in ((1, False), (5, True)):
+        x, w = randn(rows, dim, seed=dim, io=io), (1 + randn(dim, seed=1, scale=0.2, io=torch.float32)).to(io)
+        r = randn(rows, dim, seed=2, scale=3.0, io=io) if with_r else None
+        h = to64(x) + (to64(r) if with_r else 0)
+        for group in (128, None) if out == FP8 else (128,):
+            y, scales, r_out = add_rms_norm_fwd(x, w, r, out_dtype=out, group=group)
+            torch.cuda.synchronize()
+            assert y.dtype == out
+            if out == FP8:
+                assert scales.shape == ((rows, -(-dim // 128)) if group else (rows,))
+            check_out(y, scales, norm_ref(h, to64(w)), group or dim)
+            if with_r:
+                check_rounded(r_out, h, FP32_VALUE, "residual")
+            else:
+                assert r_out is None
+
+
+def test_add_rms_norm_in_place_and_shapes():
+    """The residual updated in place gives what a new one does; leading dimensions are kept."""
+    x, r, w = randn(3, 5, 512, seed=1), randn(3, 5, 512, seed=2), randn(512, seed=3)
+    y, s, r_new = add_rms_norm_fwd(x, w, r, out_dtype=FP8)
+    kept = r.clone()
+    y2, s2, r2 = add_rms_norm_fwd(x, w, kept, out_dtype=FP8, residual_out=kept)
+    torch.cuda.synchronize()
+    assert r2 is kept and torch.equal(kept, r_new) and torch.equal(s, s2)
+    assert torch.equal(y.view(torch.uint8), y2.view(torch.uint8))
+    assert y.shape == x.shape and s.shape == (3, 5, 4)
+
+
+def test_add_rms_norm_many_rows():
+    x, r, w = randn(70001, 72, seed=4), randn(70001, 72, seed=5), randn(72, seed=6)
+    y, _, r_out = add_rms_norm_fwd(x, w, r)
+    torch.cuda.synchronize()
+    h = to64(x) + to64(r)
+    check_rounded(y, norm_ref(h, to64(w)), FP32_VALUE, "y")
+    check_rounded(r_out, h, FP32_VALUE, "residual")
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last rows are normalised like the first."""
+    rows, dim = 262200, 8192
+    x = torch.zeros((rows, dim), dtype=torch.bfloat16, device=DEV)
+    x[-3:], x[:3] = randn(3, dim, seed=1), randn(3, dim, seed=2)
+    w = randn(dim, seed=3)
+    y, s, _ = add_rms_norm_fwd(x, w, out_dtype=FP8)
+    torch.cuda.synchronize()
+    for part in (slice(0, 3), slice(rows - 3, rows)):
+        check_out(y[part], s[part], norm_ref(to64(x[part]), to64(w)), 128)
+    del x, y, s
+    x = torch.zeros((rows * 64, 128), dtype=torch.bfloat16, device=DEV)
+    x[-3:] = randn(3, 128, seed=4)
+    y, _ = gated_rms_norm_fwd(x, x, randn(128, seed=5))
+    torch.cuda.synchronize()
+    h = to64(x[-3:])
+    check_rounded(y[-3:], norm_ref(h, to64(randn(128, seed=5))) * silu_ref(h), FP32_VALUE, "y")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32, FP8])
+def test_gated_rms_norm_types_and_rows(d, io, out):
+    for shape in ((1, d), (3, 5, d), (7, 37, d), (2, 33, 16, d)):
+        x, z = randn(*shape, seed=d, scale=0.3, io=io), randn(*shape, seed=2, scale=2.0, io=io)
+        w = (1 + randn(d, seed=3, scale=0.2, io=torch.float32)).to(io)
+        y, scales = gated_rms_norm_fwd(x, z, w, out_dtype=out)
+        torch.cuda.synchronize()
+        assert y.shape == x.shape and (scales is None or scales.shape == x.shape[:-1])
+        check_out(y, scales, norm_ref(to64(x), to64(w)) * silu_ref(to64(z)), d)
+
+
+def test_rows_of_zeros_and_tiny_values():
+    """A row of zeros: zeros out, scale 1.  Values whose square is below fp32's range: eps decides."""
+    x = randn(4, 256, seed=7, io=torch.float32)
+    x[1] = 0
+    x[2] *= 1e-30
+    w = torch.ones(256, device=DEV)
+    y, s, _ = add_rms_norm_fwd(x, w, out_dtype=FP8)
+    torch.cuda.synchronize()
+    assert torch.count_nonzero(y[1].float()).item() == 0 and torch.all(s[1] == 1)
+    check_out(y, s, norm_ref(to64(x), to64(w)), 128)
+    y, s = gated_rms_norm_fwd(x.view(8, 128), torch.full((8, 128), -200.0, device=DEV), w[:128], out_dtype=FP8)
+    torch.cuda.synchronize()
+    assert torch.count_nonzero(y.float()).item() == 0 and torch.isfinite(s).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_non_finite_values_stay_in_their_row(value):
+    x, w = randn(5, 384, seed=8), randn(384, seed=9)
+    clean = add_rms_norm_fwd(x, w)[0]
+    x[2, 100] = value
+    y = add_rms_norm_fwd(x, w)[0]
+    y8, s8, _ = add_rms_norm_fwd(x, w, out_dtype=FP8)
+    rows = [0, 1, 3, 4]
+    assert torch.equal(y[rows], clean[rows]) and torch.isnan(y[2, 100])
+    assert torch.isnan(y8[2, 100].float()) and torch.isfinite(y8[rows].float()).all() and torch.isfinite(s8).all()
+    z = randn(5, 384, seed=10).view(15, 128)
+    xg, wg = randn(15, 128, seed=11), w[:128].contiguous()
+    clean = gated_rms_norm_fwd(xg, z, wg)[0]
+    xg[7, 3] = value
+    y = gated_rms_norm_fwd(xg, z, wg)[0]
+    rows = [r for r in range(15) if r != 7]
+    assert torch.equal(y[rows], clean[rows]) and torch.isnan(y[7, 3])
+
+
+def test_no_rows():
+    y, s, _ = add_rms_norm_fwd(randn(0, 256), randn(256), out_dtype=FP8)
+    assert y.shape == (0, 256) and s.shape == (0, 2)
+    y, s = gated_rms_norm_fwd(randn(0, 4, 128), randn(0, 4, 128), randn(128))
+    assert y.shape == (0, 4, 128) and s is None
+
+
+def test_refusals():
+    x, w = randn(2, 256), randn(256)
+    for bad in (dict(weight=randn(255)), dict(weight=w.float()), dict(residual=randn(2, 255)), dict(out_dtype=torch.float16),
+                dict(group=64), dict(residual_out=x), dict(x=x.t().contiguous().t()), dict(x=x.to(torch.float16))):
+        with pytest.raises(ValueError):
+            add_rms_norm_fwd(**dict(dict(x=x, weight=w), **bad))
+    with pytest.raises(_lib.KktError):
+        add_rms_norm_fwd(randn(1, 16392), randn(16392))
+    with pytest.raises(_lib.KktError):
+        gated_rms_norm_fwd(randn(2, 96), randn(2, 96), randn(96))
+    with pytest.raises(ValueError):
+        gated_rms_norm_fwd(randn(2, 128), randn(2, 64), randn(128))

@@ -1,0 +1,168 @@
+"""gdn_prep_fwd (short convolution, SiLU, L2 norm, gates) against fp64, at the lengths, slots and values
+where it can go wrong (GPU)."""
+import numpy as np
+import pytest
+import torch
+
+from gdn_chunkwise_ut_gb300 import _lib, device_status, gdn_prep_fwd
+from tests.layer_compare import FP32_VALUE, check_rounded, prep_ref, to64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def make(shape, Hk, Hv, d, P, io=torch.bfloat16, taps=4, bias=True, seed=0):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    D = (2 * Hk + Hv) * d
+    randn = lambda *s: torch.randn(s, generator=gen, device=DEV)  # noqa: E731
+    return dict(x=randn(*shape, D).to(io), weight=(0.5 * randn(D, taps)).to(io), a=(2 * randn(*shape, Hv)).to(io),
+                b=randn(*shape, Hv).to(io), A_log=randn(Hv), dt_bias=randn(Hv), conv_state=randn(P, taps - 1, D).to(io),
+                bias=(0.1 * randn(D)).to(io) if bias else None, Hk=Hk, Hv=Hv, dk=d, dv=d)
+
+
+def i32(x):
+    return None if x is None else torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def run_and_check(t, slots=None, cu=None, expand=False):
+    ref = prep_ref(*(to64(t[n]) for n in ("x", "weight", "bias", "a", "b", "A_log", "dt_bias", "conv_state")),
+                   t["Hk"], t["Hv"], t["dk"], slots, cu, expand)
+    out = gdn_prep_fwd(**t, slots=i32(slots), cu_seqlens=i32(cu), expand=expand)
+    torch.cuda.synchronize()
+    assert device_status() == 0
+    for name, got, want in zip(("q", "k", "v"), out, ref):
+        check_rounded(got, want, FP32_VALUE, name)
+    # the gates value by value
+    check_rounded(out[3][..., None], ref[3][..., None], FP32_VALUE, "g")
+    check_rounded(out[4][..., None], ref[4][..., None], FP32_VALUE, "beta")
+    assert np.array_equal(to64(t["conv_state"]), ref[5])
+    return out
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("taps", [2, 3, 4])
+@pytest.mark.parametrize("d,expand", [(128, False), (64, True)])
+def test_packed_sequences_of_every_length(io, taps, d, expand):
+    """Lengths from none to 70, empty sequences first, last and in a row, short ones one behind the other
+    (the state's successor takes rows of the state itself)."""
+    lengths = [0, 1, 2, 3, 4, 5, 0, 0, 70, 1, 1, 2, 17, 3, 0]
+    cu = [int(x) for x in np.concatenate([[0], np.cumsum(lengths)])]
+    t = make((1, cu[-1]), 2, 4, d, 20, io=io, taps=taps, bias=taps != 3, seed=taps)
+    run_and_check(t, slots=[(7 * n + 3) % 20 for n in range(len(lengths))], cu=cu, expand=expand)
+
+
+@pytest.mark.parametrize("length", [1, 2, 3, 4, 5, 6, 15, 16, 17, 33])
+def test_many_sequences_of_one_length(length):
+    """Enough tokens that a warp has a run of 16: the sequences start at every place of a run, and those
+    that start near its end go on past it."""
+    n = 6000 // length
+    t = make((n, length), 1, 2, 128, n, seed=length)
+    first = {k: (v.clone() if torch.is_tensor(v) else v) for k, v in t.items()}
+    run_and_check(t)
+    # the update in place does not depend on which warp runs first
+    for _ in range(3):
+        again = {k: (v.clone() if torch.is_tensor(v) else v) for k, v in first.items()}
+        gdn_prep_fwd(**again)
+        assert torch.equal(again["conv_state"], t["conv_state"])
+
+
+@pytest.mark.parametrize("Hk,Hv,d", [(1, 1, 64), (1, 3, 64), (5, 5, 128), (16, 48, 128), (3, 6, 64)])
+def test_head_groups(Hk, Hv, d):
+    """Channel counts that do not fill the last slab, heads of q, k and v in one slab."""
+    for expand in (False, True):
+        run_and_check(make((2, 9), Hk, Hv, d, 2, seed=Hv), expand=expand)
+
+
+def test_no_slot_is_a_zero_state():
+    t = make((3, 2), 2, 2, 128, 2, seed=8)
+    run_and_check(t, slots=[1, -1, -7])
+
+
+def test_prompt_in_pieces_equals_one_call():
+    """A prompt of 50 tokens in calls of 1, 2, 3, 20 and 24: the same bits, and the same state."""
+    t = make((1, 50), 2, 4, 128, 1, seed=9)
+    one = dict(t, conv_state=t["conv_state"].clone())
+    want = gdn_prep_fwd(**one)
+    many, parts, at = t["conv_state"].clone(), [], 0
+    for n in (1, 2, 3, 20, 24):
+        cut = {k: t[k][:, at:at + n].contiguous() for k in ("x", "a", "b")}
+        parts.append(gdn_prep_fwd(**dict(t, conv_state=many, **cut)))
+        at += n
+    torch.cuda.synchronize()
+    for i in range(5):
+        assert torch.equal(torch.cat([p[i] for p in parts], 1), want[i])
+    assert torch.equal(many, one["conv_state"])
+
+
+def test_extreme_gates_and_values():
+    """Gates far out on both sides, a head of zeros (its norm is eps), large inputs."""
+    t = make((1, 6), 1, 2, 128, 1, io=torch.float32, bias=False, seed=10)
+    t["a"][0, :, 0] = torch.tensor([-200.0, -50.0, -1e-3, 1e-3, 80.0, 1000.0], device=DEV)
+    t["b"][0, :, 1] = torch.tensor([-100.0, -60.0, 0.0, 20.0, 60.0, 200.0], device=DEV)
+    t["x"][..., :128] = 0
+    t["conv_state"][..., :128] = 0
+    t["x"][..., 300] = 1e4
+    run_and_check(t)
+
+
+def test_non_finite_inputs_stay_in_their_window():
+    t = make((2, 12), 1, 1, 128, 2, seed=11)
+    clean = gdn_prep_fwd(**dict(t, conv_state=t["conv_state"].clone()))
+    x = t["x"].clone()
+    x[0, 3, 256 + 7] = float("nan")  # a channel of v: reaches tokens 3 .. 6 of that channel only
+    x[1, 5, 3] = float("inf")        # a channel of q: the head of tokens 5 .. 8
+    out = gdn_prep_fwd(**dict(t, x=x, conv_state=t["conv_state"].clone()))
+    torch.cuda.synchronize()
+    q, k, v = out[:3]
+    same = torch.ones_like(v, dtype=torch.bool)
+    same[0, 3:7, 0, 7] = False
+    assert torch.equal(v[same], clean[2][same]) and torch.isnan(v[~same]).all()
+    assert torch.equal(k, clean[1])
+    rest = [t_ for t_ in range(12) if not 5 <= t_ < 9]
+    assert torch.equal(q[0], clean[0][0]) and torch.equal(q[1, rest], clean[0][1, rest])
+
+
+def test_bad_slots_and_offsets_are_reported_not_faulted():
+    t = make((3, 20), 1, 2, 128, 4, seed=12)
+    before = t["conv_state"].clone()
+    ok = dict(t, conv_state=before.clone())
+    want = gdn_prep_fwd(**ok, slots=i32([3, 1, 0]))
+    out = gdn_prep_fwd(**t, slots=i32([3, 4, 0]))
+    torch.cuda.synchronize()
+    assert device_status() == _lib.KKT_ERR_INDEX and device_status() == 0
+    for i in range(3):
+        assert torch.equal(out[i][[0, 2]], want[i][[0, 2]])
+    assert torch.equal(t["conv_state"][[0, 3]], ok["conv_state"][[0, 3]])
+    assert torch.equal(t["conv_state"][[1, 2]], before[[1, 2]])
+    flat = dict(t, **{k: t[k].reshape(1, 60, -1) for k in ("x", "a", "b")})
+    for bad in ([0, 40, 20, 60], [1, 20, 40, 60], [0, 20, 40, 50], [0, 20, 40, 1 << 30], [0, -5, 40, 60]):
+        gdn_prep_fwd(**flat, cu_seqlens=i32(bad))
+        torch.cuda.synchronize()
+        assert device_status() == _lib.KKT_ERR_SEQLENS, bad
+
+
+def test_no_tokens():
+    t = make((1, 0), 2, 2, 128, 2)
+    before = t["conv_state"].clone()
+    out = gdn_prep_fwd(**t, cu_seqlens=i32([0, 0, 0]))
+    torch.cuda.synchronize()
+    assert out[0].shape == (1, 0, 2, 128) and torch.equal(t["conv_state"], before)
+
+
+def test_refusals():
+    t = make((2, 3), 2, 4, 128, 2)
+    gdn_prep_fwd(**t)
+    for bad in (dict(Hv=3), dict(weight=t["weight"].float()), dict(a=t["a"].float()), dict(A_log=t["A_log"].double()),
+                dict(bias=t["bias"][:-1]), dict(conv_state=t["conv_state"][:, :2].contiguous()),
+                dict(x=t["x"].to(torch.float16)), dict(x=t["x"][..., ::2])):
+        with pytest.raises(ValueError):
+            gdn_prep_fwd(**dict(t, **bad))
+    with pytest.raises(_lib.KktError):
+        gdn_prep_fwd(**make((2, 3), 2, 3, 128, 2))       # 3 value heads for 2 key heads
+    with pytest.raises(_lib.KktError):
+        gdn_prep_fwd(**make((2, 3), 2, 4, 32, 2))        # head dimension
+    with pytest.raises(_lib.KktError):
+        gdn_prep_fwd(**make((2, 3), 2, 4, 64, 2, taps=5))
+    with pytest.raises(_lib.KktError):
+        gdn_prep_fwd(**make((3, 3), 2, 4, 64, 2))        # three sequences, two slots, none named

@@ -1,0 +1,226 @@
+"""gdn_recurrent_fwd (the gated delta rule token by token over a pool of states) against the fp64
+token-by-token oracle, at the sizes, slots and values where it can go wrong (GPU)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import gdn
+from gdn_chunkwise_ut_gb300 import _lib, chunk_gated_delta_rule, device_status, gdn_recurrent_fwd
+from gdn_chunkwise_ut_gb300.inputs import make_gate, make_inputs, make_query, make_state
+from tests.compare import check_recurrence
+from tests.layer_compare import FP32_STATE, check_rounded, spans, to64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def make(shape, Hk, Hv, dk, dv, io=torch.bfloat16, gated=True, P=4, state=torch.float32, seed=0):
+    B, T = shape
+    k, _, _ = make_inputs(B, T, Hk, dk, dk, seed=seed, dtype=io, device=DEV)
+    _, v, beta = make_inputs(B, T, Hv, dv, dv, seed=seed + 1, dtype=io, device=DEV)
+    q = make_query(B, T, Hk, dk, seed=seed, device=DEV).to(io)
+    g = make_gate(B, T, Hv, seed=seed, device=DEV) if gated else None
+    return q, k, v, beta, g, make_state(P, Hv, dk, dv, seed=seed, device=DEV).to(state)
+
+
+def reference(q, k, v, beta, g, state, slots, slots_out, cu, scale):
+    """(o, pool) in fp64: each sequence through the oracle from its slot's state."""
+    Hk, Hv = q.shape[2], v.shape[2]
+    q, k, v, beta, g, pool = (to64(x) for x in (q, k, v, beta, g, state))
+    q, k = np.repeat(q, Hv // Hk, 2), np.repeat(k, Hv // Hk, 2)
+    flat = [None if x is None else x.reshape(1, -1, *x.shape[2:]) for x in (q, k, v, beta, g)]
+    o, new = np.zeros_like(flat[2]), pool.copy()
+    for n, (s, e) in enumerate(spans(v.shape, cu)):
+        a = n if slots is None else int(slots[n])
+        z = a if slots_out is None else int(slots_out[n])
+        S = pool[a] if a >= 0 else np.zeros(pool.shape[1:])
+        if e > s:
+            part = [None if x is None else x[:, s:e] for x in flat]
+            o[:, s:e], S = gdn.recurrent_fwd(*part, initial_state=S[None], scale=scale)
+            S = S[0]
+        if z >= 0:
+            new[z] = S
+    return o.reshape(v.shape), new
+
+
+def run_and_check(q, k, v, beta, g, state, slots=None, slots_out=None, cu=None, scale=None, **kw):
+    d = q.shape[-1]
+    o_ref, pool_ref = reference(q, k, v, beta, g, state, slots, slots_out, cu, d ** -0.5 if scale is None else scale)
+    named = set(range(len(spans(v.shape, cu)))) if slots is None and slots_out is None else \
+        {int(s) for s in (slots if slots_out is None else slots_out)}
+    before = state.clone()
+    i32 = lambda x: None if x is None else torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    o = torch.full_like(v, float("nan"))
+    got = gdn_recurrent_fwd(q, k, v, beta, state, g=g, slots=i32(slots), slots_out=i32(slots_out), cu_seqlens=i32(cu),
+                            scale=scale, o=o, **kw)
+    torch.cuda.synchronize()
+    assert device_status() == 0 and got is o
+    check_rounded(o, o_ref, FP32_STATE, "o")
+    check_rounded(state, pool_ref, FP32_STATE, "state")
+    for s in set(range(state.shape[0])) - named:  # slots that no sequence writes
+        assert torch.equal(state[s], before[s])
+    return o
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("state", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (128, 64), (64, 128)])
+def test_single_tokens_and_short_runs(io, state, dk, dv):
+    for T in (1, 2, 5):
+        run_and_check(*make((3, T), 2, 4, dk, dv, io=io, state=state, P=5, seed=T), slots=[4, 0, 2])
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_packed_sequences_of_every_length(gated):
+    """Lengths 0, 1, 2, 63, 100 and 7 packed, with empty ones first, last and in a row."""
+    lengths = [0, 1, 2, 0, 0, 63, 100, 7, 0]
+    cu = [int(x) for x in np.concatenate([[0], np.cumsum(lengths)])]
+    args = make((1, cu[-1]), 3, 3, 128, 128, gated=gated, P=12, seed=3)
+    run_and_check(*args, slots=[11, 3, 5, 7, 1, 0, 9, 2, 10], cu=cu, scale=0.3)
+
+
+def test_slots_in_and_out():
+    """A state read from one slot and written to another (a fork with its first tokens), an empty sequence
+    moved, a sequence that starts from no state, one whose state is not kept."""
+    cu = [0, 3, 3, 4, 9]
+    args = make((1, 9), 1, 2, 128, 128, P=8, seed=5)
+    run_and_check(*args, slots=[2, 2, -1, 3], slots_out=[4, 5, 6, -1], cu=cu)
+    args = make((4, 1), 1, 2, 128, 128, P=8, seed=6)
+    run_and_check(*args, slots=[7, -1, -5, 0])
+
+
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (1, 7), (5, 5), (4, 12)])
+def test_head_groups(Hk, Hv):
+    run_and_check(*make((2, 3), Hk, Hv, 64, 128, P=2, seed=Hv))
+
+
+def test_default_slots_are_the_identity():
+    run_and_check(*make((3, 1), 2, 2, 128, 128, P=6))
+
+
+def test_agrees_with_the_chunked_form():
+    """130 tokens through both forms, within the chunked form's tolerances."""
+    q, k, v, beta, g, S0 = make((2, 130), 3, 3, 128, 128, P=2, seed=9)
+    o, S = chunk_gated_delta_rule(q, k, v, g, beta, initial_state=S0, output_final_state=True)
+    state = S0.clone()
+    o1 = gdn_recurrent_fwd(q, k, v, beta, state, g=g)
+    torch.cuda.synchronize()
+    check_recurrence(to64(o), to64(o1), to64(S), to64(state))
+
+
+def test_a_call_a_token_equals_one_call():
+    """Decode steps carry on from the state exactly: 6 calls of one token give the bits of one of six."""
+    q, k, v, beta, g, S0 = make((3, 6), 2, 4, 128, 128, P=3, seed=10)
+    one, many = S0.clone(), S0.clone()
+    o1 = gdn_recurrent_fwd(q, k, v, beta, one, g=g)
+    o2 = torch.cat([gdn_recurrent_fwd(*(x[:, t:t + 1].contiguous() for x in (q, k, v, beta)), many,
+                                      g=g[:, t:t + 1].contiguous()) for t in range(6)], 1)
+    torch.cuda.synchronize()
+    assert torch.equal(o1, o2) and torch.equal(one, many)
+
+
+def test_large_pool_offsets():
+    """Slots past 2^31 elements of the pool."""
+    P, Hv = 2200, 64  # 64 x 128 x 128 values a slot: 2^20, 2.3e9 in all
+    state = torch.zeros((P, Hv, 128, 128), dtype=torch.bfloat16, device=DEV)
+    q, k, v, beta, g, S0 = make((2, 1), 16, Hv, 128, 128, P=2, state=torch.bfloat16, seed=4)
+    state[P - 1], state[3] = S0[0], S0[1]
+    o = gdn_recurrent_fwd(q, k, v, beta, state, g=g, slots=torch.tensor([P - 1, 3], dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    o_ref, new = reference(q, k, v, beta, g, S0, None, None, None, 128 ** -0.5)
+    check_rounded(o, o_ref, FP32_STATE, "o")
+    check_rounded(state[[P - 1, 3]], new, FP32_STATE, "state")
+    assert torch.count_nonzero(state[:3]).item() == 0 and torch.count_nonzero(state[2000:P - 1]).item() == 0
+
+
+def test_non_finite_values_stay_in_their_sequence():
+    q, k, v, beta, g, state = make((3, 2), 2, 2, 128, 128, P=3, seed=12)
+    clean = state.clone()
+    ref = gdn_recurrent_fwd(q, k, v, beta, clean, g=g)
+    v2, st2 = v.clone(), state.clone()
+    v2[1, 0, 0, 5] = float("nan")
+    st2[1, 1, 3, 7] = float("inf")
+    o = gdn_recurrent_fwd(q, k, v2, beta, st2, g=g)
+    torch.cuda.synchronize()
+    for n in (0, 2):
+        assert torch.equal(o[n], ref[n]) and torch.equal(st2[n], clean[n])
+    # columns are independent: only column 5 of head 0 and column 7 of head 1 are touched
+    keep = torch.ones(128, dtype=torch.bool, device=DEV)
+    keep[5] = False
+    assert torch.equal(st2[1, 0][:, keep], clean[1, 0][:, keep]) and torch.isnan(st2[1, 0, :, 5]).all()
+    assert not torch.isfinite(st2[1, 1, :, 7]).any()
+
+
+def test_a_strong_decay_forgets_the_state():
+    """g = -200 (e^g is 0 in fp32): the state is the last token's own, without NaN."""
+    q, k, v, beta, g, state = make((1, 3), 1, 1, 128, 128, P=1, seed=13)
+    run_and_check(q, k, v, beta, torch.full_like(g, -200.0), state)
+
+
+def test_bad_slots_and_offsets_are_reported_not_faulted():
+    q, k, v, beta, g, state = make((3, 1), 2, 2, 128, 128, P=4, seed=14)
+    before, ok = state.clone(), state.clone()
+    ref = gdn_recurrent_fwd(q, k, v, beta, ok, g=g, slots=torch.tensor([3, 1, 0], dtype=torch.int32, device=DEV))
+    o = gdn_recurrent_fwd(q, k, v, beta, state, g=g, slots=torch.tensor([3, 4, 0], dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    assert device_status() == _lib.KKT_ERR_INDEX and device_status() == 0
+    assert torch.equal(o[[0, 2]], ref[[0, 2]]) and torch.equal(state[[0, 3]], ok[[0, 3]])
+    assert torch.equal(state[[1, 2]], before[[1, 2]])
+    with pytest.raises(_lib.KktError, match="slot index"):
+        gdn_recurrent_fwd(q, k, v, beta, state, g=g, slots=torch.tensor([3, 9, 0], dtype=torch.int32, device=DEV),
+                          check=True)
+    flat = [x.reshape(1, 3, *x.shape[2:]) for x in (q, k, v, beta)]
+    for bad in ([0, 2, 1, 3], [1, 2, 3, 3], [0, 1, 2, 2], [0, 1, 2, 1 << 30]):
+        gdn_recurrent_fwd(*flat, state, cu_seqlens=torch.tensor(bad, dtype=torch.int32, device=DEV))
+        torch.cuda.synchronize()
+        assert device_status() == _lib.KKT_ERR_SEQLENS
+
+
+def test_on_another_stream_and_in_a_graph():
+    q, k, v, beta, g, S0 = make((2, 1), 2, 4, 128, 128, P=3, seed=15)
+    slots = torch.tensor([2, 0], dtype=torch.int32, device=DEV)
+    want = S0.clone()
+    o1 = gdn_recurrent_fwd(q, k, v, beta, want, g=g, slots=slots)
+    o2 = gdn_recurrent_fwd(q, k, v, beta, want, g=g, slots=slots)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    state = S0.clone()
+    stream.wait_stream(torch.cuda.current_stream())
+    got = gdn_recurrent_fwd(q, k, v, beta, state, g=g, slots=slots, stream=stream)
+    stream.synchronize()
+    assert torch.equal(got, o1)
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out = gdn_recurrent_fwd(q, k, v, beta, state, g=g, slots=slots)
+    state.copy_(S0)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, o1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, o2) and torch.equal(state, want)
+
+
+def test_refusals():
+    q, k, v, beta, g, state = make((2, 1), 2, 4, 128, 128, P=2)
+    ok = dict(g=g)
+    gdn_recurrent_fwd(q, k, v, beta, state, **ok)
+    for bad in (dict(k=k[:, :, :1].contiguous()), dict(v=v.float()), dict(beta=beta.to(torch.bfloat16)),
+                dict(state=state.to(torch.float16)), dict(state=state[:, :2].contiguous()), dict(q=q.transpose(0, 1)),
+                dict(v=v.cpu())):
+        a = dict(q=q, k=k, v=v, beta=beta, state=state)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            gdn_recurrent_fwd(**a, **ok)
+    with pytest.raises(ValueError):
+        gdn_recurrent_fwd(q, k, v, beta, state, g=g, slots=torch.tensor([0, 1], device=DEV))  # int64
+    with pytest.raises(ValueError):
+        gdn_recurrent_fwd(q, k, v, beta, state, g=g, cu_seqlens=torch.tensor([0, 1], dtype=torch.int32, device=DEV))
+    with pytest.raises(_lib.KktError):  # more sequences than slots, and no slots named
+        gdn_recurrent_fwd(q, k, v, beta, state[:1], g=g)
+    with pytest.raises(_lib.KktError):  # 4 value heads are not a multiple of 3
+        gdn_recurrent_fwd(*make((2, 1), 3, 4, 128, 128, P=2)[:4], state)
+    with pytest.raises(_lib.KktError):
+        gdn_recurrent_fwd(*make((2, 1), 2, 4, 32, 32, P=2)[:4], make_state(2, 4, 32, 32, device=DEV))

@@ -1,0 +1,154 @@
+"""gdn_state_copy and StatePool (GPU): copies, forks, clears, compaction, bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+from gdn_chunkwise_ut_gb300 import StatePool, _lib, device_status, gdn_state_copy
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device=DEV)
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8).cpu().numpy().reshape(t.shape[0], -1)
+
+
+def pools(P, seed=0):
+    """Pools of every kind of slot: large, small, of an odd number of bytes, of one value; a NaN's bits too."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    out = [torch.randn((P, 3, 128, 128), generator=gen, device=DEV),
+           torch.randn((P, 3, 320), generator=gen, device=DEV).to(torch.bfloat16),
+           torch.randn((P, 7, 5), generator=gen, device=DEV).to(torch.bfloat16),
+           torch.randint(0, 255, (P, 1), generator=gen, device=DEV, dtype=torch.uint8),
+           torch.randn((P, 4099), generator=gen, device=DEV)]
+    out[0][0, 0, 0, 0] = float("nan")
+    return out
+
+
+def expect(src, dst, src_slots, dst_slots):
+    want = [bits(d).copy() for d in dst]
+    for w, s in zip(want, src if src is not None else [None] * len(dst)):
+        from_ = None if s is None else bits(s)
+        for m, d in enumerate(dst_slots):
+            if d >= 0:
+                w[d] = 0 if from_ is None or src_slots[m] < 0 else from_[src_slots[m]]
+    return want
+
+
+def test_moves_forks_and_clears_in_place():
+    t = pools(12)
+    src, dst = [3, 3, 3, 0, -1, 7, 5], [1, 2, 11, 4, 6, -1, 8]
+    want = expect(t, t, src, dst)
+    gdn_state_copy(t, i32(dst), t, i32(src))
+    torch.cuda.synchronize()
+    assert device_status() == 0
+    for got, w in zip(t, want):
+        assert np.array_equal(bits(got), w)
+
+
+def test_between_pools_and_clear():
+    a, b = pools(5, 1), pools(9, 2)
+    src, dst = [4, 0, 2], [8, 3, 0]
+    want = expect(a, b, src, dst)
+    gdn_state_copy(b, i32(dst), a, i32(src))
+    torch.cuda.synchronize()
+    for got, w in zip(b, want):
+        assert np.array_equal(bits(got), w)
+    want = expect(None, a, None, [1, 4])
+    gdn_state_copy(a, i32([1, 4]))
+    gdn_state_copy(a[0], i32([]))
+    torch.cuda.synchronize()
+    for got, w in zip(a, want):
+        assert np.array_equal(bits(got), w)
+
+
+def test_strided_slots_and_odd_places():
+    """A layer's part of a larger tensor, and pools that do not start on a 16-byte boundary."""
+    whole = torch.randn((6, 4, 130), device=DEV)
+    before = whole.clone()
+    part = whole[:, 1]
+    gdn_state_copy(part, i32([5, 0]), part, i32([2, 3]))
+    raw = torch.randn(6 * 64 + 1, device=DEV)
+    odd = raw[1:].view(6, 64)
+    kept = odd.clone()
+    gdn_state_copy(odd, i32([1]), odd, i32([4]))
+    torch.cuda.synchronize()
+    before[5, 1], before[0, 1] = before[2, 1].clone(), before[3, 1].clone()
+    kept[1] = kept[4]
+    assert torch.equal(whole, before) and torch.equal(odd, kept)
+
+
+def test_offsets_past_32_bits():
+    P = 1100
+    t = torch.zeros((P, 1 << 20), dtype=torch.float32, device=DEV)  # 4.6e9 bytes
+    t[3] = torch.arange(1 << 20, device=DEV)
+    gdn_state_copy(t, i32([P - 1]), t, i32([3]))
+    gdn_state_copy(t, i32([7]), t, i32([P - 1]))
+    torch.cuda.synchronize()
+    assert torch.equal(t[P - 1], t[3]) and torch.equal(t[7], t[3])
+    assert torch.count_nonzero(t).item() == 3 * ((1 << 20) - 1)
+
+
+def test_more_moves_than_a_grid_holds():
+    n = 70000
+    t = torch.zeros((2 * n, 4), device=DEV)
+    t[:n] = torch.randn((n, 4), device=DEV)
+    gdn_state_copy(t, torch.arange(n, 2 * n, device=DEV, dtype=torch.int32), t,
+                   torch.arange(n, device=DEV, dtype=torch.int32).flip(0).contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(t[n:], t[:n].flip(0))
+
+
+def test_bad_slots_are_reported_not_faulted():
+    t = torch.randn((4, 64), device=DEV)
+    before = t.clone()
+    for dst, src in (([4, 1], [0, 2]), ([3, 1], [9, 2])):
+        t.copy_(before)
+        gdn_state_copy(t, i32(dst), t, i32(src))
+        torch.cuda.synchronize()
+        assert device_status() == _lib.KKT_ERR_INDEX
+        assert torch.equal(t[1], before[2]) and torch.equal(t[[0, 2, 3]], before[[0, 2, 3]])
+
+
+def test_refusals():
+    t = torch.zeros((4, 64), device=DEV)
+    for bad in (dict(dst=[]), dict(dst=[t] * 65), dict(dst_slots=i32([0]).long()), dict(src_slots=i32([0])),
+                dict(src=t), dict(src=t, src_slots=i32([0, 1])), dict(src=t.double(), src_slots=i32([0])),
+                dict(src=[t, t], src_slots=i32([0])), dict(dst=t.cpu()), dict(dst=t.t()),
+                dict(dst=t[:1].expand(4, 64)), dict(dst=[t, torch.zeros((5, 64), device=DEV)]),
+                dict(dst=torch.zeros(4, device=DEV))):
+        with pytest.raises(ValueError):
+            gdn_state_copy(**dict(dict(dst=t, dst_slots=i32([0])), **bad))
+
+
+def test_pool_fork_free_compact():
+    pool = StatePool(6, 2, 1, 2, 64, 64)
+    a, b, c = pool.alloc(3)
+    for l in range(2):
+        for s in (a, b, c):
+            pool.states[l][s] = 10 * s + l + 1
+            pool.convs[l][s] = 10 * s + l + 5
+    forks = pool.fork(b, 2)
+    pool.free([a, b])
+    moves = pool.compact()
+    at = lambda s: moves.get(s, s)  # noqa: E731
+    torch.cuda.synchronize()
+    assert sorted([at(c), *map(at, forks)]) == [0, 1, 2]
+    for l in range(2):
+        assert torch.all(pool.states[l][at(c)] == 10 * c + l + 1) and torch.all(pool.convs[l][at(c)] == 10 * c + l + 5)
+        for f in forks:
+            assert torch.all(pool.states[l][at(f)] == 10 * b + l + 1)
+            assert torch.all(pool.convs[l][at(f)] == 10 * b + l + 5)
+    new = pool.alloc(3)
+    torch.cuda.synchronize()
+    assert new == [3, 4, 5]
+    assert all(torch.count_nonzero(t[new]).item() == 0 for t in pool.states + pool.convs)
+    with pytest.raises(ValueError):
+        pool.fork(17)
+    with pytest.raises(RuntimeError):
+        pool.alloc()

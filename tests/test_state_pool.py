@@ -1,0 +1,51 @@
+"""The bookkeeping of a state pool's slots (CPU): which are live, what a compaction moves."""
+import random
+
+import pytest
+
+from gdn_chunkwise_ut_gb300 import SlotTable
+
+
+def test_lowest_free_slots_first_and_all_or_none():
+    t = SlotTable(5)
+    assert t.alloc(3) == [0, 1, 2] and len(t) == 3 and t.free_slots == 2
+    with pytest.raises(RuntimeError):
+        t.alloc(3)
+    assert t.free_slots == 2  # nothing was taken
+    t.free([1])
+    assert t.alloc(2) == [1, 3] and t.alloc(0) == []
+
+
+def test_refusals():
+    t = SlotTable(4)
+    t.alloc(2)
+    for bad in ([2], [0, 0], [-1], [7]):
+        with pytest.raises(ValueError):
+            t.free(bad)
+    assert len(t) == 2
+    t.free([0])
+    with pytest.raises(ValueError):
+        t.free([0])
+    with pytest.raises(ValueError):
+        t.alloc(-1)
+    with pytest.raises(ValueError):
+        SlotTable(0)
+
+
+def test_compact_moves_are_independent_and_keep_every_state():
+    rng = random.Random(3)
+    for _ in range(200):
+        n = rng.randrange(1, 40)
+        t = SlotTable(n)
+        held = {s: object() for s in t.alloc(rng.randrange(0, n + 1))}
+        for s in list(held):
+            if rng.random() < 0.5:
+                t.free([s])
+                del held[s]
+        moves = t.compact()
+        assert not set(moves) & set(moves.values())          # no move reads what another writes
+        assert all(new < old for old, new in moves.items())
+        after = {moves.get(s, s): x for s, x in held.items()}
+        assert sorted(after) == list(range(len(held)))       # nothing lost, the lowest slots
+        assert all(t.is_live(s) for s in after) and len(t) == len(held) and t.free_slots == n - len(held)
+        assert t.alloc(t.free_slots) == list(range(len(held), n))
