@@ -1,4 +1,5 @@
-"""ctypes declarations of libkkt.so (the C ABI in include/kkt.h).
+"""ctypes declarations of libkkt.so (the C ABI in include/kkt.h and include/gdn_layer.h), and the
+native binding of the serving operators.
 
 Argument marshalling only.  If the library is missing, every entry point
 raises: there is no Python or CPU fallback.
@@ -6,6 +7,7 @@ raises: there is no Python or CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().parent / "_build" / "libkkt.so"
@@ -91,6 +93,25 @@ def lib(path: Path | None = None):
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         _lib = _declare(ctypes.CDLL(str(LIB_PATH)))
     return _lib
+
+
+_binding = None
+
+
+def binding():
+    """The native binding of the serving operators, linked against libkkt.so (raises if it has not been built)."""
+    global _binding
+    if _binding is None:
+        lib()
+        path = LIB_PATH.with_name("_gdn_binding.so")
+        if not path.exists():
+            raise RuntimeError(f"the binding is not built ({path}); run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_file_location("_gdn_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding = module
+    return _binding
 
 
 def _declare(l):

@@ -127,3 +127,38 @@ def test_copy_argument_errors(lib):
         assert call(**bad) == _lib.KKT_ERR_ARG, bad
     assert call(dslots=0x5002) == _lib.KKT_ERR_ALIGN and call(sslots=0x6001) == _lib.KKT_ERR_ALIGN
     assert call(m=0) == _lib.KKT_OK
+
+
+def test_binding_refuses_host_tensors(lib):
+    """The native binding's checks, without a GPU: ValueError, nothing launched."""
+    import torch
+
+    from gdn_chunkwise_ut_gb300 import (add_rms_norm_fwd, gated_rms_norm_fwd, gdn_prep_fwd, gdn_recurrent_fwd,
+                                        gdn_state_copy)
+    x = torch.zeros((1, 1, 2, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn_recurrent_fwd(x, x, x, torch.zeros((1, 1, 2)), torch.zeros((1, 2, 128, 128)))
+    with pytest.raises(ValueError, match="expected"):
+        gdn_recurrent_fwd(x[0], x, x, torch.zeros((1, 1, 2)), torch.zeros((1, 2, 128, 128)))
+    with pytest.raises(ValueError, match="channels"):
+        gdn_prep_fwd(x[0], x[0, 0], x[0], x[0], x[0, 0, 0], x[0, 0, 0], x[0], Hk=1, Hv=1, dk=64, dv=64)
+    with pytest.raises(ValueError, match="integer"):
+        gdn_prep_fwd(x[0], x[0, 0], x[0], x[0], x[0, 0, 0], x[0, 0, 0], x[0], Hk=1.5, Hv=1, dk=64, dv=64)
+    with pytest.raises(ValueError, match="CUDA"):
+        add_rms_norm_fwd(x, x[0, 0, 0])
+    with pytest.raises(ValueError, match="CUDA"):
+        gated_rms_norm_fwd(x, None, x[0, 0, 0])
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn_state_copy([x], torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="list of tensors"):
+        gdn_state_copy(3, torch.zeros(1, dtype=torch.int32))
+
+
+def test_missing_binding_fails_loudly(lib, monkeypatch, tmp_path):
+    import torch
+
+    from gdn_chunkwise_ut_gb300 import add_rms_norm_fwd
+    monkeypatch.setattr(_lib, "LIB_PATH", tmp_path / "libkkt.so")
+    monkeypatch.setattr(_lib, "_binding", None)
+    with pytest.raises(RuntimeError, match="binding is not built"):
+        add_rms_norm_fwd(torch.zeros((1, 8)), torch.zeros(8))
