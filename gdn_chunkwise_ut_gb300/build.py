@@ -122,7 +122,7 @@ def _link_binding(started) -> None:
     libs = Path(torch.__file__).parent / "lib"
     tmp = BUILD / f"binding.{os.getpid()}.tmp.so"
     subprocess.run(["g++", "-shared", "-o", str(tmp), str(obj), f"-L{BUILD}", "-l:libkkt.so", f"-L{libs}",
-                    "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], check=True)
+                    "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], check=True)
     os.replace(tmp, BINDING)
 
 

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -77,7 +78,7 @@ void *raw(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 CUstream_st *stream_on(c10::Device dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
 Tensor empty(at::IntArrayRef shape, ScalarType dtype, c10::Device dev) {
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(dev));
+    return at::detail::empty_cuda(shape, dtype, dev, std::nullopt);
 }
 
 int small(int64_t v, const char *name) {

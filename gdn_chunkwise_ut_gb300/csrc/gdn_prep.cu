@@ -7,6 +7,16 @@
 // channels in registers, so a run reads every input once (plus three before its first token).  A
 // head's sum of squares is a shuffle over its 8 or 16 lanes.  The two gates are one more slab.
 //
+// What bounds it: by bytes HBM (the 27.9k packed tokens of 6144 channels of the bf16 prefill case
+// move 686 MB, 103 us at the copy rate; it takes 128 us, 80%), but 25 output heads' worth of SiLU and
+// norms a token keep the issue slots half busy, so the kernel is written against latency:
+//   - the inputs go through a ring of rows in shared memory by asynchronous copies, nine rows ahead,
+//     each lane reading back what it copied itself (no barrier), so that no registers wait on memory;
+//   - three tokens, the window's turn, are computed side by side, and pairs of channels share one
+//     fp32 instruction (128 us; one token after the other 140 us, with scalar arithmetic 192 us);
+//   - 8 channels a lane in 128 registers, 16 warps an SM (4 channels a lane: twice the warps, but more
+//     instructions a channel, 157 us); blocks of two warps, since a block's idle warps hold registers.
+//
 // The convolution's state is read, and its successor written, by the warp that has the sequence's
 // first token, whichever run holds the last one: the same thread reads and writes each element, so
 // updating the pool in place needs no order between warps.  For that, the tokens whose window reaches
@@ -19,8 +29,10 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kPrepWarps = 8;
-constexpr int kPrepBatch = 4;  // tokens whose inputs are loaded together
+constexpr int kPrepWarps = 2;
+constexpr int kPrepBatch = 3;   // tokens whose inputs are copied together: the window's turn
+constexpr int kPrepStages = 4;  // such copies in flight, with the one in use
+static_assert(kPrepBatch == 3, "the window's registers take turns with the tokens of a batch");
 constexpr int kSlab = 256;     // channels of a warp
 
 struct PrepParams {
@@ -29,7 +41,7 @@ struct PrepParams {
     const int32_t *cu, *slots;
     void *conv_state, *q, *k, *v;
     float *g, *beta;
-    int N, T, Hk, Hv, D, taps, expand, run, num_slots, slabs;
+    int N, T, Hk, Hv, D, taps, expand, run, num_slots, slabs, wide_weights;
     int64_t ntok;
     float eps;
     int *status;
@@ -37,10 +49,10 @@ struct PrepParams {
 
 // The sequence of token t: the last one that starts at or before it (empty ones before it are passed
 // over).  False, with the error recorded, where cu_seqlens is malformed there.
-__device__ __forceinline__ bool seq_of_token(const PrepParams &p, int64_t t, int &n, int64_t &a, int64_t &b) {
+__device__ __forceinline__ bool seq_of_token(const PrepParams &p, int t, int &n, int &a, int &b) {
     if (!p.cu) {
-        n = (int)(t / p.T);
-        a = (int64_t)n * p.T;
+        n = t / p.T;
+        a = n * p.T;
         b = a + p.T;
         return true;
     }
@@ -51,8 +63,8 @@ __device__ __forceinline__ bool seq_of_token(const PrepParams &p, int64_t t, int
     }
     n = lo;
     const Span s = seq_span(p.cu, n, p.N, p.T, p.ntok, p.status);
-    a = s.a;
-    b = s.b;
+    a = (int)s.a;
+    b = (int)s.b;
     if (s.ok && (t < a || t >= b)) {
         record_error(p.status, KKT_ERR_SEQLENS);
         return false;
@@ -73,17 +85,43 @@ __device__ __forceinline__ void gates(const PrepParams &p, int64_t first, int64_
     }
 }
 
+// Copies of a lane's 8 channels of one row into its own place in shared memory, read back by the same
+// lane, so that a wait for the lane's own copies is all the ordering there is.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// x / (1 + e^-x) of a pair.
+__device__ __forceinline__ float2 silu2(float2 x) {
+    const float2 t = mul2(x, make_float2(-1.44269504f, -1.44269504f));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(1.f + e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(1.f + e.y));
+    return mul2(x, r);
+}
+
 template <typename IO, int DH>
-__global__ void __launch_bounds__(kPrepWarps * 32) gdn_prep_kernel(const PrepParams p) {
+__global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const PrepParams p) {
+    extern __shared__ __align__(16) uint8_t smem[];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int slab = blockIdx.y * kPrepWarps + (threadIdx.x >> 5);
-    const int64_t t0 = (int64_t)blockIdx.x * p.run;
-    const int64_t t1 = t0 + p.run < p.ntok ? t0 + p.run : p.ntok;
+    // tokens are counted in 32 bits (there are fewer than 2^31)
+    const int ntok = (int)p.ntok;
+    const int t0 = (int)blockIdx.x * p.run;
+    const int t1 = ntok - t0 < p.run ? ntok : t0 + p.run;
     if (slab > p.slabs) return;
     if (slab == p.slabs) {
-        gates<IO>(p, t0 * p.Hv, (t1 - t0) * p.Hv, lane);
+        gates<IO>(p, (int64_t)t0 * p.Hv, (int64_t)(t1 - t0) * p.Hv, lane);
         if (blockIdx.x == 0 && p.cu)
             for (int n = lane; n < p.N; n += 32) check_sequence(p.cu, n, p.N, p.ntok, p.status);
         return;
@@ -92,22 +130,76 @@ __global__ void __launch_bounds__(kPrepWarps * 32) gdn_prep_kernel(const PrepPar
     const bool live = ch < p.D;  // the last slab may be short
     const int chc = live ? ch : 0;
     const int keep = p.taps - 1;
+    const IO *x = static_cast<const IO *>(p.x) + chc;
+
+    // this warp's tokens [t, end)
+    int n = 0, a = 0, b = 0;
+    int t = t0, end = t1;
+    bool ok = seq_of_token(p, t0, n, a, b);
+    if (keep > 1) {
+        if (ok && t0 > a && t0 - a < keep) t = b - a > keep ? a + keep : b;
+        int la = a, lb = b;  // the last token's sequence
+        bool lok = ok;
+        if (!ok || b < t1) {
+            int ln;
+            lok = seq_of_token(p, t1 - 1, ln, la, lb);
+        }
+        if (lok && la >= t0 && lb > t1 && t1 - la < keep) end = lb - la > keep ? la + keep : lb;
+    }
+    if (t >= end) return;
+
+    uint8_t *ring = smem + ((threadIdx.x >> 5) * kPrepStages * kPrepBatch * 32 + lane) * (8 * sizeof(IO));
+    constexpr int kRowBytes = 32 * 8 * sizeof(IO);
+    const int64_t D = p.D;
+    // rows [from, from + kPrepBatch) into a stage
+    auto fetch = [&](int from, int stage) {
+        uint8_t *d = ring + stage * (kPrepBatch * kRowBytes);
+        const IO *src = x + from * D;
+#pragma unroll
+        for (int i = 0; i < kPrepBatch; ++i)
+            if (i < end - from) {
+                copy16_async(d + i * kRowBytes, src + i * D);
+                if constexpr (sizeof(IO) == 4) copy16_async(d + i * kRowBytes + 16, src + i * D + 4);
+            }
+        copy_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kPrepStages - 1; ++s) fetch(t + s * kPrepBatch, s);
 
     // weights, in front of them zeros where there are fewer than four taps
-    float w[4][8], bias[8];
+    float2 w[4][4], bias[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int e = 0; e < 4; ++e) {
+        const IO *wr = static_cast<const IO *>(p.weight) + (int64_t)(chc + 2 * e) * p.taps;
+        float f[2][4] = {};
+        if (p.taps == 4 && p.wide_weights) {
+            float v[8];
+            widen8(raw8(wr), v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int tap = j - (4 - p.taps);
-            w[j][e] = tap >= 0 ? to_f32(static_cast<const IO *>(p.weight)[(int64_t)(chc + e) * p.taps + tap]) : 0.f;
+            for (int j = 0; j < 8; ++j) f[j >> 2][j & 3] = v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int tap = j - (4 - p.taps);
+                if (tap >= 0) {
+                    f[0][j] = to_f32(wr[tap]);
+                    f[1][j] = to_f32(wr[p.taps + tap]);
+                }
+            }
         }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) bias[e] = p.bias ? to_f32(static_cast<const IO *>(p.bias)[chc + e]) : 0.f;
+        for (int j = 0; j < 4; ++j) w[j][e] = make_float2(f[0][j], f[1][j]);
+        bias[e] = make_float2(0.f, 0.f);
+        if (p.bias) {
+            const IO *br = static_cast<const IO *>(p.bias) + chc + 2 * e;
+            bias[e] = make_float2(to_f32(br[0]), to_f32(br[1]));
+        }
+    }
 
     // where this lane's head goes
     const int head = chc / DH;
     const bool norm = head < 2 * p.Hk;
+    const bool any_norm = __any_sync(0xffffffffu, norm);
     const int rep = p.Hv / p.Hk;
     IO *dst;
     int64_t dst_stride;
@@ -124,105 +216,159 @@ __global__ void __launch_bounds__(kPrepWarps * 32) gdn_prep_kernel(const PrepPar
         dst_stride = (int64_t)p.Hv * DH;
     }
 
-    const IO *x = static_cast<const IO *>(p.x) + chc;
-    float win[3][8];  // the three inputs before the current token, oldest first
+    // The three inputs before the current token: before a batch's token i the oldest is win[i % 3],
+    // which takes the token's own input in its place.
+    float2 win[3][4];
+    // The sequence of token tt, the batch's token i, begins (or the run does): the inputs before it,
+    // and, with the first token, the state that the sequence leaves.
+    auto enter = [&](int tt, int i) {
+        if (!ok) b = tt + 1;  // this token alone is passed over
+        int slot = -1;
+        if (ok) slot = slot_of(p.slots, n, p.num_slots, p.status, ok);
+        const int pos = tt - a;
+        IO *state = static_cast<IO *>(p.conv_state) + (int64_t)slot * keep * p.D + chc;
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
+        for (int j = 0; j < 3; ++j) {
+            const int back = 3 - j;  // the input `back` tokens before this one
+            float2(&before)[4] = win[(i + j) % 3];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) win[j][e] = 0.f;
-
-    int n = 0;
-    int64_t a = 0, b = -1;
-    int slot = -1;
-    bool ok = false;
-    int64_t t = t0, end = t1;
-    if (keep > 1 && seq_of_token(p, t0, n, a, b) && t0 > a && t0 < a + keep) t = a + keep < b ? a + keep : b;
-    b = -1;  // the loop looks its first token up itself
-    while (t < end) {
-        const int count = end - t < kPrepBatch ? (int)(end - t) : kPrepBatch;
-        Raw8<IO> in[kPrepBatch];
-#pragma unroll
-        for (int i = 0; i < kPrepBatch; ++i)
-            if (i < count) in[i] = raw8(x + (t + i) * p.D);
-#pragma unroll
-        for (int i = 0; i < kPrepBatch; ++i) {
-            if (i >= count) break;
-            const int64_t tt = t + i;
-            if (tt >= b) {
-                // a new sequence (or the run's first token): the inputs before it
-                ok = seq_of_token(p, tt, n, a, b);
-                if (!ok) b = tt + 1;  // this token alone is passed over
-                slot = -1;
-                if (ok) slot = slot_of(p.slots, n, p.num_slots, p.status, ok);
-                if (ok) {
-                    const int64_t pos = tt - a;
-                    IO *state = static_cast<IO *>(p.conv_state) + (int64_t)slot * keep * p.D + chc;
-#pragma unroll
-                    for (int j = 0; j < 3; ++j) {
-                        const int back = 3 - j;  // the input `back` tokens before this one
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) win[j][e] = 0.f;
-                        if (back <= keep) {
-                            if (pos >= back) widen8(raw8(x + (tt - back) * p.D), win[j]);
-                            else if (slot >= 0) widen8(raw8(state + (keep + pos - back) * p.D), win[j]);
-                        }
-                    }
-                    if (pos == 0 && a + keep > t1 && b > t1) end = a + keep < b ? a + keep : b;
-                    if (pos == 0 && slot >= 0 && live) {
-                        // the state the sequence leaves: the last `keep` of the old state and its inputs,
-                        // oldest first, so that an old row is read before it is overwritten
-                        const int64_t len = b - a;
-                        for (int r = 0; r < keep; ++r) {
-                            const int64_t from = len + r;
-                            const Raw8<IO> row = from < keep ? raw8(state + from * p.D) : raw8(x + (a + from - keep) * p.D);
-                            float f[8];
-                            widen8(row, f);
-                            store8(state + (int64_t)r * p.D, f);
-                        }
-                    }
-                }
-            }
-            float cur[8], y[8];
-            widen8(in[i], cur);
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float acc = fmaf(win[0][e], w[0][e], bias[e]);
-                acc = fmaf(win[1][e], w[1][e], acc);
-                acc = fmaf(win[2][e], w[2][e], acc);
-                acc = fmaf(cur[e], w[3][e], acc);
-                y[e] = silu(acc);
-                ss = fmaf(y[e], y[e], ss);
-                win[0][e] = win[1][e];
-                win[1][e] = win[2][e];
-                win[2][e] = cur[e];
-            }
-            ss = lanes_sum<DH / 8>(ss);
-            if (norm) {
-                const float r = rsqrtf(ss + p.eps);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] *= r;
-            }
-            if (live && ok) {
-                IO *o = dst + tt * dst_stride;
-                for (int c = 0; c < copies; ++c) store8(o + c * DH, y);
+            for (int e = 0; e < 4; ++e) before[e] = make_float2(0.f, 0.f);
+            if (ok && back <= keep) {
+                if (pos >= back) widen8(raw8(x + (tt - back) * D), before);
+                else if (slot >= 0) widen8(raw8(state + (keep + pos - back) * D), before);
             }
         }
-        t += count;
+        if (ok && pos == 0 && slot >= 0 && live) {
+            // the last `keep` of the old state and the sequence's inputs, oldest first, so that an old
+            // row is read before it is overwritten
+            const int len = b - a;
+            for (int r = 0; r < keep; ++r) {
+                const int from = len + r;
+                const Raw8<IO> row = from < keep ? raw8(state + from * D) : raw8(x + (a + from - keep) * D);
+                float f[8];
+                widen8(row, f);
+                store8(state + r * D, f);
+            }
+        }
+    };
+    const uint8_t *rows = ring;  // of the batch in use
+    // The batch's token i: its input from the ring, its output to memory where `store` says so.
+    auto token = [&](int i, IO *o, bool store) {
+        float2 cur[4], y[4];
+        widen8(raw8(reinterpret_cast<const IO *>(rows + i * kRowBytes)), cur);
+        float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float2 acc = fma2(win[i % 3][e], w[0][e], bias[e]);
+            acc = fma2(win[(i + 1) % 3][e], w[1][e], acc);
+            acc = fma2(win[(i + 2) % 3][e], w[2][e], acc);
+            y[e] = silu2(fma2(cur[e], w[3][e], acc));
+            win[i % 3][e] = cur[e];
+        }
+        if (any_norm) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ss = fma2(y[e], y[e], ss);
+            const float total = lanes_sum<DH / 8>(ss.x + ss.y);
+            const float r = norm ? rsqrtf(total + p.eps) : 1.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], make_float2(r, r));
+        }
+        if (store) {
+            store8(o, y);
+            for (int c = 1; c < copies; ++c) store8(o + c * DH, y);
+        }
+    };
+    if (t == b) ok = seq_of_token(p, t, n, a, b);
+    enter(t, 0);
+    int stage = 0;
+    IO *o = dst + t * dst_stride;
+    for (; t < end; t += kPrepBatch) {
+        fetch(t + (kPrepStages - 1) * kPrepBatch, stage == 0 ? kPrepStages - 1 : stage - 1);
+        copy_wait<kPrepStages - 1>();
+        rows = ring + stage * (kPrepBatch * kRowBytes);
+        if (t + kPrepBatch <= (b < end ? b : end)) {
+            // the batch lies in one sequence: its tokens side by side, without checks between them
+            float2 y[kPrepBatch][4];
+#pragma unroll
+            for (int i = 0; i < kPrepBatch; ++i) {
+                float2 cur[4];
+                widen8(raw8(reinterpret_cast<const IO *>(rows + i * kRowBytes)), cur);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 acc = fma2(win[i % 3][e], w[0][e], bias[e]);
+                    acc = fma2(win[(i + 1) % 3][e], w[1][e], acc);
+                    acc = fma2(win[(i + 2) % 3][e], w[2][e], acc);
+                    y[i][e] = fma2(cur[e], w[3][e], acc);
+                    win[i % 3][e] = cur[e];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPrepBatch; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[i][e] = silu2(y[i][e]);
+            if (any_norm) {
+                float ss[kPrepBatch];
+#pragma unroll
+                for (int i = 0; i < kPrepBatch; ++i) {
+                    float2 s2 = mul2(y[i][0], y[i][0]);
+#pragma unroll
+                    for (int e = 1; e < 4; ++e) s2 = fma2(y[i][e], y[i][e], s2);
+                    ss[i] = s2.x + s2.y;
+                }
+#pragma unroll
+                for (int m = DH / 16; m > 0; m >>= 1)
+#pragma unroll
+                    for (int i = 0; i < kPrepBatch; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], m);
+#pragma unroll
+                for (int i = 0; i < kPrepBatch; ++i) {
+                    const float r = norm ? rsqrtf(ss[i] + p.eps) : 1.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], make_float2(r, r));
+                }
+            }
+            if (live && ok) {
+#pragma unroll
+                for (int i = 0; i < kPrepBatch; ++i) store8(o + i * dst_stride, y[i]);
+                for (int c = 1; c < copies; ++c)
+#pragma unroll
+                    for (int i = 0; i < kPrepBatch; ++i) store8(o + i * dst_stride + c * DH, y[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPrepBatch; ++i) {
+                if (t + i >= end) break;
+                if (t + i >= b) {
+                    ok = seq_of_token(p, t + i, n, a, b);
+                    enter(t + i, i);
+                }
+                token(i, o + i * dst_stride, live && ok);
+            }
+        }
+        o += kPrepBatch * dst_stride;
+        stage = stage + 1 < kPrepStages ? stage + 1 : 0;
     }
+}
+
+template <typename IO, int DH>
+int launch(const PrepParams &p, dim3 grid, cudaStream_t st) {
+    constexpr int smem = kPrepWarps * kPrepStages * kPrepBatch * 32 * 8 * (int)sizeof(IO);
+    if (!ensure_max_smem<gdn_prep_kernel<IO, DH>>(smem)) return KKT_ERR_CUDA;
+    return launch_serialised(gdn_prep_kernel<IO, DH>, grid, kPrepWarps * 32, smem, st, p);
 }
 
 template <typename IO>
 int launch(PrepParams &p, int dh, cudaStream_t st) {
     p.slabs = (p.D + kSlab - 1) / kSlab;
-    // Tokens of a run: a longer run re-reads fewer of the three inputs before it, a shorter one gives
-    // more warps.  16 (19% re-reads, from the caches) once that leaves 8 warps for every SM.
-    const int64_t want = (int64_t)sm_count_cached() * 8;
-    p.run = 16;
-    while (p.run > 1 && (p.ntok + p.run - 1) / p.run * (p.slabs + 1) < want) p.run /= 4;
+    p.wide_weights = aligned_ptr(p.weight, 16);
+    // Tokens of a run: a longer run re-reads fewer of the three inputs before it and loads its weights
+    // less often, a shorter one gives more warps: the longest that still fills the SMs (16 warps each).
+    // In the prefill case (see the top) runs of 36 tokens take 130 us, 48 128, 96 134; in decode, a
+    // token a sequence, runs of one keep each sequence's chain of loads on a warp of its own.
+    const int64_t want = (int64_t)sm_count_cached() * 16;
+    p.run = 48;
+    while (p.run > 1 && (p.ntok + p.run - 1) / p.run * (p.slabs + 1) < want) p.run = p.run > 3 ? p.run / 2 : 1;
     const dim3 grid((unsigned)((p.ntok + p.run - 1) / p.run), (unsigned)((p.slabs + 1 + kPrepWarps - 1) / kPrepWarps));
-    return dh == 128 ? launch_serialised(gdn_prep_kernel<IO, 128>, grid, kPrepWarps * 32, 0, st, p)
-                     : launch_serialised(gdn_prep_kernel<IO, 64>, grid, kPrepWarps * 32, 0, st, p);
+    return dh == 128 ? launch<IO, 128>(p, grid, st) : launch<IO, 64>(p, grid, st);
 }
 
 }  // namespace
@@ -239,7 +385,7 @@ extern "C" int gdn_prep_fwd(const void *x, const void *weight, const void *bias,
     if (dk != dv || (dk != 64 && dk != 128) || taps < 2 || taps > 4) return KKT_ERR_UNSUPPORTED;
     const int64_t ntok = cu_seqlens ? (int64_t)T : (int64_t)N * T;
     const int64_t D = ((int64_t)2 * Hk + Hv) * dk;
-    if (ntok > 0x7fffffffLL || D > (int64_t)kSlab * 65535) return KKT_ERR_ARG;
+    if (ntok > 0x7fffff00LL || D > (int64_t)kSlab * 65535) return KKT_ERR_ARG;  // room for a batch past the end
     if (!weight || !A_log || !dt_bias) return KKT_ERR_ARG;
     if (ntok > 0 && (!x || !a || !b || !q || !k || !v || !g || !beta)) return KKT_ERR_ARG;
     if (num_slots > 0 && !conv_state) return KKT_ERR_ARG;
