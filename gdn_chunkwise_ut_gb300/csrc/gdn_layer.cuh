@@ -77,6 +77,13 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ void store_raw8(float *p, const Raw8<float> &r) {
+    *reinterpret_cast<float4 *>(p) = r.a;
+    *reinterpret_cast<float4 *>(p + 4) = r.b;
+}
+__device__ __forceinline__ void store_raw8(__nv_bfloat16 *p, const Raw8<__nv_bfloat16> &r) {
+    *reinterpret_cast<uint4 *>(p) = r.a;
+}
 // In 8 bits; values past the type's largest are held at it (a NaN stays one).
 __device__ __forceinline__ void store8(__nv_fp8_e4m3 *p, const float (&v)[8]) {
     uint32_t w[2];

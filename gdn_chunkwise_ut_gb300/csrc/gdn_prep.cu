@@ -108,6 +108,104 @@ __device__ __forceinline__ float2 silu2(float2 x) {
     return mul2(x, r);
 }
 
+// Weights and bias of the 8 channels from ch on, in front of the weights zeros where there are fewer
+// than four taps.
+template <typename IO>
+__device__ __forceinline__ void load_weights(const PrepParams &p, int ch, float2 (&w)[4][4], float2 (&bias)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const IO *wr = static_cast<const IO *>(p.weight) + (int64_t)(ch + 2 * e) * p.taps;
+        float f[2][4] = {};
+        if (p.taps == 4 && p.wide_weights) {
+            float v[8];
+            widen8(raw8(wr), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j >> 2][j & 3] = v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int tap = j - (4 - p.taps);
+                if (tap >= 0) {
+                    f[0][j] = to_f32(wr[tap]);
+                    f[1][j] = to_f32(wr[p.taps + tap]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j][e] = make_float2(f[0][j], f[1][j]);
+        bias[e] = make_float2(0.f, 0.f);
+        if (p.bias) {
+            const IO *br = static_cast<const IO *>(p.bias) + ch + 2 * e;
+            bias[e] = make_float2(to_f32(br[0]), to_f32(br[1]));
+        }
+    }
+}
+
+// Where a lane's channels of a token go: `copies` places, DH apart, from dst + token * stride on;
+// the heads of q and k are normalised (any: some lane's of the warp).
+template <typename IO>
+struct HeadOut {
+    IO *dst;
+    int64_t stride;
+    int copies;
+    bool norm, any;
+};
+template <typename IO, int DH>
+__device__ __forceinline__ HeadOut<IO> head_out(const PrepParams &p, int ch) {
+    HeadOut<IO> h;
+    const int head = ch / DH;
+    h.norm = head < 2 * p.Hk;
+    h.any = __any_sync(0xffffffffu, h.norm);
+    h.copies = 1;
+    if (h.norm) {
+        const int rep = p.expand ? p.Hv / p.Hk : 1;
+        const int j = head < p.Hk ? head : head - p.Hk;
+        h.dst = static_cast<IO *>(head < p.Hk ? p.q : p.k) + (int64_t)j * rep * DH + ch % DH;
+        h.stride = (int64_t)p.Hk * rep * DH;
+        h.copies = rep;
+    } else {
+        h.dst = static_cast<IO *>(p.v) + (int64_t)(head - 2 * p.Hk) * DH + ch % DH;
+        h.stride = (int64_t)p.Hv * DH;
+    }
+    return h;
+}
+
+// SiLU, the norm where the head has one, and the stores, of B tokens side by side.
+template <typename IO, int DH, int B>
+__device__ __forceinline__ void finish(const PrepParams &p, const HeadOut<IO> &h, float2 (&y)[B][4], IO *o, bool store) {
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[i][e] = silu2(y[i][e]);
+    if (h.any) {
+        float ss[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            float2 s2 = mul2(y[i][0], y[i][0]);
+#pragma unroll
+            for (int e = 1; e < 4; ++e) s2 = fma2(y[i][e], y[i][e], s2);
+            ss[i] = s2.x + s2.y;
+        }
+#pragma unroll
+        for (int m = DH / 16; m > 0; m >>= 1)
+#pragma unroll
+            for (int i = 0; i < B; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], m);
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const float r = h.norm ? rsqrtf(ss[i] + p.eps) : 1.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], make_float2(r, r));
+        }
+    }
+    if (store) {
+#pragma unroll
+        for (int i = 0; i < B; ++i) store8(o + i * h.stride, y[i]);
+        for (int c = 1; c < h.copies; ++c)
+#pragma unroll
+            for (int i = 0; i < B; ++i) store8(o + i * h.stride + c * DH, y[i]);
+    }
+}
+
 template <typename IO, int DH>
 __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const PrepParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -166,55 +264,9 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
 #pragma unroll
     for (int s = 0; s < kPrepStages - 1; ++s) fetch(t + s * kPrepBatch, s);
 
-    // weights, in front of them zeros where there are fewer than four taps
     float2 w[4][4], bias[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const IO *wr = static_cast<const IO *>(p.weight) + (int64_t)(chc + 2 * e) * p.taps;
-        float f[2][4] = {};
-        if (p.taps == 4 && p.wide_weights) {
-            float v[8];
-            widen8(raw8(wr), v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j >> 2][j & 3] = v[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int tap = j - (4 - p.taps);
-                if (tap >= 0) {
-                    f[0][j] = to_f32(wr[tap]);
-                    f[1][j] = to_f32(wr[p.taps + tap]);
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j][e] = make_float2(f[0][j], f[1][j]);
-        bias[e] = make_float2(0.f, 0.f);
-        if (p.bias) {
-            const IO *br = static_cast<const IO *>(p.bias) + chc + 2 * e;
-            bias[e] = make_float2(to_f32(br[0]), to_f32(br[1]));
-        }
-    }
-
-    // where this lane's head goes
-    const int head = chc / DH;
-    const bool norm = head < 2 * p.Hk;
-    const bool any_norm = __any_sync(0xffffffffu, norm);
-    const int rep = p.Hv / p.Hk;
-    IO *dst;
-    int64_t dst_stride;
-    int copies = 1;
-    if (norm) {
-        const int j = head < p.Hk ? head : head - p.Hk;
-        dst = static_cast<IO *>(head < p.Hk ? p.q : p.k);
-        const int ho = p.expand ? j * rep : j;
-        dst_stride = (int64_t)(p.expand ? p.Hv : p.Hk) * DH;
-        dst += (int64_t)ho * DH + chc % DH;
-        if (p.expand) copies = rep;
-    } else {
-        dst = static_cast<IO *>(p.v) + (int64_t)(head - 2 * p.Hk) * DH + chc % DH;
-        dst_stride = (int64_t)p.Hv * DH;
-    }
+    load_weights<IO>(p, chc, w, bias);
+    const HeadOut<IO> out = head_out<IO, DH>(p, chc);
 
     // The three inputs before the current token: before a batch's token i the oldest is win[i % 3],
     // which takes the token's own input in its place.
@@ -252,36 +304,23 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
         }
     };
     const uint8_t *rows = ring;  // of the batch in use
-    // The batch's token i: its input from the ring, its output to memory where `store` says so.
-    auto token = [&](int i, IO *o, bool store) {
-        float2 cur[4], y[4];
+    // The convolution at the batch's token i, its input from the ring.
+    auto convolve = [&](int i, float2(&y)[4]) {
+        float2 cur[4];
         widen8(raw8(reinterpret_cast<const IO *>(rows + i * kRowBytes)), cur);
-        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float2 acc = fma2(win[i % 3][e], w[0][e], bias[e]);
             acc = fma2(win[(i + 1) % 3][e], w[1][e], acc);
             acc = fma2(win[(i + 2) % 3][e], w[2][e], acc);
-            y[e] = silu2(fma2(cur[e], w[3][e], acc));
+            y[e] = fma2(cur[e], w[3][e], acc);
             win[i % 3][e] = cur[e];
-        }
-        if (any_norm) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) ss = fma2(y[e], y[e], ss);
-            const float total = lanes_sum<DH / 8>(ss.x + ss.y);
-            const float r = norm ? rsqrtf(total + p.eps) : 1.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], make_float2(r, r));
-        }
-        if (store) {
-            store8(o, y);
-            for (int c = 1; c < copies; ++c) store8(o + c * DH, y);
         }
     };
     if (t == b) ok = seq_of_token(p, t, n, a, b);
     enter(t, 0);
     int stage = 0;
-    IO *o = dst + t * dst_stride;
+    IO *o = out.dst + t * out.stride;
     for (; t < end; t += kPrepBatch) {
         fetch(t + (kPrepStages - 1) * kPrepBatch, stage == 0 ? kPrepStages - 1 : stage - 1);
         copy_wait<kPrepStages - 1>();
@@ -290,49 +329,8 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
             // the batch lies in one sequence: its tokens side by side, without checks between them
             float2 y[kPrepBatch][4];
 #pragma unroll
-            for (int i = 0; i < kPrepBatch; ++i) {
-                float2 cur[4];
-                widen8(raw8(reinterpret_cast<const IO *>(rows + i * kRowBytes)), cur);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float2 acc = fma2(win[i % 3][e], w[0][e], bias[e]);
-                    acc = fma2(win[(i + 1) % 3][e], w[1][e], acc);
-                    acc = fma2(win[(i + 2) % 3][e], w[2][e], acc);
-                    y[i][e] = fma2(cur[e], w[3][e], acc);
-                    win[i % 3][e] = cur[e];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kPrepBatch; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[i][e] = silu2(y[i][e]);
-            if (any_norm) {
-                float ss[kPrepBatch];
-#pragma unroll
-                for (int i = 0; i < kPrepBatch; ++i) {
-                    float2 s2 = mul2(y[i][0], y[i][0]);
-#pragma unroll
-                    for (int e = 1; e < 4; ++e) s2 = fma2(y[i][e], y[i][e], s2);
-                    ss[i] = s2.x + s2.y;
-                }
-#pragma unroll
-                for (int m = DH / 16; m > 0; m >>= 1)
-#pragma unroll
-                    for (int i = 0; i < kPrepBatch; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], m);
-#pragma unroll
-                for (int i = 0; i < kPrepBatch; ++i) {
-                    const float r = norm ? rsqrtf(ss[i] + p.eps) : 1.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], make_float2(r, r));
-                }
-            }
-            if (live && ok) {
-#pragma unroll
-                for (int i = 0; i < kPrepBatch; ++i) store8(o + i * dst_stride, y[i]);
-                for (int c = 1; c < copies; ++c)
-#pragma unroll
-                    for (int i = 0; i < kPrepBatch; ++i) store8(o + i * dst_stride + c * DH, y[i]);
-            }
+            for (int i = 0; i < kPrepBatch; ++i) convolve(i, y[i]);
+            finish<IO, DH>(p, out, y, o, live && ok);
         } else {
 #pragma unroll
             for (int i = 0; i < kPrepBatch; ++i) {
@@ -341,12 +339,64 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
                     ok = seq_of_token(p, t + i, n, a, b);
                     enter(t + i, i);
                 }
-                token(i, o + i * dst_stride, live && ok);
+                float2 y[1][4];
+                convolve(i, y[0]);
+                finish<IO, DH>(p, out, y, o + i * out.stride, live && ok);
             }
         }
-        o += kPrepBatch * dst_stride;
+        o += kPrepBatch * out.stride;
         stage = stage + 1 < kPrepStages ? stage + 1 : 0;
     }
+}
+
+// A decode step, one token for every sequence: a warp has one sequence's token, with nothing to slide
+// over.  The state's rows wait for the slot alone; everything else is loaded beside it.
+template <typename IO, int DH>
+__global__ void __launch_bounds__(kPrepWarps * 32) gdn_prep_step_kernel(const PrepParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int slab = blockIdx.y * kPrepWarps + (threadIdx.x >> 5);
+    const int n = blockIdx.x;
+    if (slab > p.slabs) return;
+    if (slab == p.slabs) {
+        gates<IO>(p, (int64_t)n * p.Hv, p.Hv, lane);
+        return;
+    }
+    bool ok = true;
+    const int slot = slot_of(p.slots, n, p.num_slots, p.status, ok);
+    const int ch = slab * kSlab + lane * 8;
+    const bool live = ch < p.D;
+    const int chc = live ? ch : 0;
+    const int64_t D = p.D;
+    const Raw8<IO> in = raw8(static_cast<const IO *>(p.x) + n * D + chc);
+    float2 w[4][4], y[1][4];
+    load_weights<IO>(p, chc, w, y[0]);
+    const int keep = p.taps - 1;
+    float2 cur[4];
+    if (ok && slot >= 0) {
+        IO *state = static_cast<IO *>(p.conv_state) + (int64_t)slot * keep * D + chc;
+        Raw8<IO> row[3];
+#pragma unroll
+        for (int r = 0; r < 3; ++r)
+            if (r < keep) row[r] = raw8(state + r * D);
+#pragma unroll
+        for (int r = 0; r < 3; ++r)
+            if (r < keep) {
+                widen8(row[r], cur);
+                const int j = r + 4 - p.taps;  // the row's tap
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[0][e] = fma2(cur[e], j == 0 ? w[0][e] : j == 1 ? w[1][e] : w[2][e], y[0][e]);
+                // the rows move up by one, the token's input behind them
+                if (live) store_raw8(state + r * D, r + 1 < keep ? row[r + 1] : in);
+            }
+    }
+    // the token's own tap last, as in a longer run: a prompt and its decode steps round alike
+    widen8(in, cur);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[0][e] = fma2(cur[e], w[3][e], y[0][e]);
+    const HeadOut<IO> out = head_out<IO, DH>(p, chc);
+    finish<IO, DH>(p, out, y, out.dst + n * out.stride, live && ok);
 }
 
 template <typename IO, int DH>
@@ -362,12 +412,17 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
     p.wide_weights = aligned_ptr(p.weight, 16);
     // Tokens of a run: a longer run re-reads fewer of the three inputs before it and loads its weights
     // less often, a shorter one gives more warps: the longest that still fills the SMs (16 warps each).
-    // In the prefill case (see the top) runs of 36 tokens take 130 us, 48 128, 96 134; in decode, a
-    // token a sequence, runs of one keep each sequence's chain of loads on a warp of its own.
+    // In the prefill case (see the top) runs of 36 tokens take 130 us, 48 128, 96 134.
+    const unsigned blocks = (unsigned)((p.slabs + 1 + kPrepWarps - 1) / kPrepWarps);
+    if (!p.cu && p.T == 1) {
+        const dim3 grid((unsigned)p.N, blocks);
+        return dh == 128 ? launch_serialised(gdn_prep_step_kernel<IO, 128>, grid, kPrepWarps * 32, 0, st, p)
+                         : launch_serialised(gdn_prep_step_kernel<IO, 64>, grid, kPrepWarps * 32, 0, st, p);
+    }
     const int64_t want = (int64_t)sm_count_cached() * 16;
     p.run = 48;
     while (p.run > 1 && (p.ntok + p.run - 1) / p.run * (p.slabs + 1) < want) p.run = p.run > 3 ? p.run / 2 : 1;
-    const dim3 grid((unsigned)((p.ntok + p.run - 1) / p.run), (unsigned)((p.slabs + 1 + kPrepWarps - 1) / kPrepWarps));
+    const dim3 grid((unsigned)((p.ntok + p.run - 1) / p.run), blocks);
     return dh == 128 ? launch<IO, 128>(p, grid, st) : launch<IO, 64>(p, grid, st);
 }
 

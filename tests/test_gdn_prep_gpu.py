@@ -67,6 +67,40 @@ def test_many_sequences_of_one_length(length):
         assert torch.equal(again["conv_state"], t["conv_state"])
 
 
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("taps", [2, 3, 4])
+@pytest.mark.parametrize("Hk,Hv,d", [(2, 4, 128), (1, 3, 64), (5, 5, 64)])
+def test_decode_steps(io, taps, Hk, Hv, d):
+    """One token a sequence, four steps on end, slots scattered and missing, as one call of four tokens."""
+    t = make((6, 4), Hk, Hv, d, 9, io=io, taps=taps, bias=taps != 4, seed=20 + taps)
+    slots = [8, 0, -1, 3, 5, 2]
+    many = dict(t, conv_state=t["conv_state"].clone())
+    want = run_and_check(t, slots=slots, expand=taps == 3)
+    for s in range(4):
+        step = dict(many, **{k: t[k][:, s:s + 1].contiguous() for k in ("x", "a", "b")})
+        ref_state = step["conv_state"].clone()
+        out = run_and_check(step, slots=slots, expand=taps == 3)
+        rows = [0, 1, 3, 4, 5]  # the sequence without a slot starts from zeros at every step
+        for i in range(5):
+            assert torch.equal(out[i][rows, 0], want[i][rows, s])
+        assert torch.equal(step["conv_state"][[1, 4, 6, 7]], ref_state[[1, 4, 6, 7]])
+    assert torch.equal(many["conv_state"], t["conv_state"])
+
+
+def test_decode_step_with_a_bad_slot():
+    t = make((3, 1), 2, 2, 64, 4, seed=31)
+    before = t["conv_state"].clone()
+    ok = dict(t, conv_state=before.clone())
+    want = gdn_prep_fwd(**ok, slots=i32([3, 1, 0]))
+    out = gdn_prep_fwd(**t, slots=i32([3, 4, 0]))
+    torch.cuda.synchronize()
+    assert device_status() == _lib.KKT_ERR_INDEX and device_status() == 0
+    for i in range(5):
+        assert torch.equal(out[i][[0, 2]], want[i][[0, 2]])
+    assert torch.equal(t["conv_state"][[0, 3]], ok["conv_state"][[0, 3]])
+    assert torch.equal(t["conv_state"][[1, 2]], before[[1, 2]])
+
+
 @pytest.mark.parametrize("Hk,Hv,d", [(1, 1, 64), (1, 3, 64), (5, 5, 128), (16, 48, 128), (3, 6, 64)])
 def test_head_groups(Hk, Hv, d):
     """Channel counts that do not fill the last slab, heads of q, k and v in one slab."""
