@@ -143,8 +143,20 @@ __device__ __forceinline__ void store8(T *p, const float2 (&v)[4]) {
     store8(p, f);
 }
 
-// x / (1 + e^-x) by the hardware's exponential and reciprocal: a few parts in 10^7.
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// x / (1 + e^-x) of a pair, by the hardware's exponential and reciprocal: a few parts in 10^7.
+__device__ __forceinline__ float2 silu2(float2 x) {
+    const float2 t = mul2(x, make_float2(-1.44269504f, -1.44269504f));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    return mul2(x, make_float2(rcp_approx(1.f + e.x), rcp_approx(1.f + e.y)));
+}
 
 // Sum (maximum) over aligned groups of W lanes.
 template <int W>
@@ -160,10 +172,13 @@ __device__ __forceinline__ float lanes_max(float x) {
     return x;
 }
 
-// The scale that takes a group's largest magnitude to the 8-bit type's largest value.  A group of
-// zeros has 1; below 2^-126 the scale stays a normal number, so that its reciprocal is finite.
-__device__ __forceinline__ float e4m3_scale(float top) {
-    return top > 0.f ? fmaxf(__fdiv_rn(top, 448.f), 1.17549435e-38f) : 1.f;
+// The scale that takes a group's largest magnitude to the 8-bit type's largest value, and its
+// reciprocal, each within two units in the last place.  A group of zeros has 1; below 2^-126 the scale
+// stays a normal number, so that its reciprocal is finite.
+__device__ __forceinline__ float e4m3_scale(float top, float &inv) {
+    const float s = top > 0.f ? fmaxf(top * (1.f / 448.f), 1.17549435e-38f) : 1.f;
+    inv = rcp_approx(s);
+    return s;
 }
 
 // Tokens [a, b) of sequence n; ok is false (and the error recorded) where cu_seqlens is malformed.

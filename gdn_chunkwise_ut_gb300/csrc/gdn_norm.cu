@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(NV == 4 ? 512 : 256) add_rms_norm_kernel(const
 #pragma unroll
             for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(h[j][e]));
             if (p.group) {
-                const float s = e4m3_scale(lanes_max<16>(m)), inv = 1.f / s;
+                float inv;
+                const float s = e4m3_scale(lanes_max<16>(m), inv);
                 const int e = e0 + j * step;
                 if ((threadIdx.x & 15) == 0 && e < p.dim)
                     p.scales[(int64_t)blockIdx.x * ((p.dim + 127) / 128) + e / 128] = s;
@@ -115,7 +116,8 @@ __global__ void __launch_bounds__(NV == 4 ? 512 : 256) add_rms_norm_kernel(const
     }
     if constexpr (sizeof(OUT) == 1) {
         if (!p.group) {
-            const float s = e4m3_scale(block_reduce<true>(top, part[1], warps)), inv = 1.f / s;
+            float inv;
+            const float s = e4m3_scale(block_reduce<true>(top, part[1], warps), inv);
             if (threadIdx.x == 0) p.scales[blockIdx.x] = s;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(NV == 4 ? 512 : 256) add_rms_norm_kernel(const
     for (int j = 0; j < NV; ++j) row_store<VEC>(static_cast<OUT *>(p.y) + at, e0 + j * step, p.dim, h[j]);
 }
 
-// DIM / 8 lanes a row, kRows rows to a thread, so that their loads are in flight together.
+// DIM / 8 lanes a row, kGatedRows rows to a thread, whose loads are in flight together.
 constexpr int kGatedRows = 4;
 template <typename IO, typename OUT, int DIM>
 __global__ void __launch_bounds__(256) gated_rms_norm_kernel(const NormParams p) {
@@ -136,42 +138,39 @@ __global__ void __launch_bounds__(256) gated_rms_norm_kernel(const NormParams p)
     griddep_wait();
     const int e = (threadIdx.x % L) * 8;
     const int64_t row0 = (int64_t)blockIdx.x * (PER * kGatedRows) + threadIdx.x / L;
-    float w[8];
+    const int left = (int)(p.rows - row0 < PER * kGatedRows ? p.rows - row0 : PER * kGatedRows);  // may be negative
+    float2 w[4];
     widen8(raw8(static_cast<const IO *>(p.w) + e), w);
-    Raw8<IO> xr[kGatedRows], zr[kGatedRows];
+    const IO *px = static_cast<const IO *>(p.x) + row0 * DIM + e, *pz = static_cast<const IO *>(p.z) + row0 * DIM + e;
+    Raw8<IO> xr[kGatedRows] = {}, zr[kGatedRows] = {};
 #pragma unroll
-    for (int i = 0; i < kGatedRows; ++i) {
-        const int64_t row = row0 + i * PER;
-        if (row < p.rows) {
-            xr[i] = raw8(static_cast<const IO *>(p.x) + row * DIM + e);
-            zr[i] = raw8(static_cast<const IO *>(p.z) + row * DIM + e);
-        } else {
-            xr[i] = Raw8<IO>{};
-            zr[i] = Raw8<IO>{};
+    for (int i = 0; i < kGatedRows; ++i)
+        if (i * PER < left) {
+            xr[i] = raw8(px + i * PER * DIM);
+            zr[i] = raw8(pz + i * PER * DIM);
         }
-    }
 #pragma unroll
     for (int i = 0; i < kGatedRows; ++i) {
-        const int64_t row = row0 + i * PER;
-        float x[8], z[8];
+        const bool live = i * PER < left;
+        float2 x[4], z[4];
         widen8(xr[i], x);
         widen8(zr[i], z);
-        float ss = 0.f;
+        float2 ss = mul2(x[0], x[0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-        const float r = rsqrtf(lanes_sum<L>(ss) / (float)DIM + p.eps);
+        for (int j = 1; j < 4; ++j) ss = fma2(x[j], x[j], ss);
+        const float r = rsqrtf(lanes_sum<L>(ss.x + ss.y) * (1.f / DIM) + p.eps);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j] * silu(z[j]);
+        for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(mul2(x[j], make_float2(r, r)), w[j]), silu2(z[j]));
         if constexpr (sizeof(OUT) == 1) {
-            float m = 0.f;
+            float m = 0.f, inv;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
-            const float s = e4m3_scale(lanes_max<L>(m)), inv = 1.f / s;
-            if (e == 0 && row < p.rows) p.scales[row] = s;
+            for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
+            const float s = e4m3_scale(lanes_max<L>(m), inv);
+            if (e == 0 && live) p.scales[row0 + i * PER] = s;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= inv;
+            for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], make_float2(inv, inv));
         }
-        if (row < p.rows) store8(static_cast<OUT *>(p.y) + row * DIM + e, x);
+        if (live) store8(static_cast<OUT *>(p.y) + row0 * DIM + e + i * PER * DIM, x);
     }
 }
 

@@ -96,18 +96,6 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// x / (1 + e^-x) of a pair.
-__device__ __forceinline__ float2 silu2(float2 x) {
-    const float2 t = mul2(x, make_float2(-1.44269504f, -1.44269504f));
-    float2 e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-    float2 r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(1.f + e.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(1.f + e.y));
-    return mul2(x, r);
-}
-
 // Weights and bias of the 8 channels from ch on, in front of the weights zeros where there are fewer
 // than four taps.
 template <typename IO>
