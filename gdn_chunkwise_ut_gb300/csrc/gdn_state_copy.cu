@@ -18,6 +18,7 @@ struct CopyTensor {
 };
 struct CopyParams {
     CopyTensor t[GDN_COPY_MAX_TENSORS];
+    unsigned end[GDN_COPY_MAX_TENSORS];  // pieces of a move up to and with tensor i
     const int32_t *dst_slots, *src_slots;
     int dst_num, src_num;
     int *status;
@@ -26,9 +27,10 @@ struct CopyParams {
 __global__ void __launch_bounds__(kCopyThreads) state_copy_kernel(const __grid_constant__ CopyParams p) {
     griddep_launch_dependents();
     griddep_wait();
-    const CopyTensor &t = p.t[blockIdx.z];
-    const size_t first = (size_t)blockIdx.x * kCopyPiece;
-    if (first >= t.bytes) return;
+    int i = 0;
+    while (blockIdx.x >= p.end[i]) ++i;  // blockIdx.x is below the last tensor's end
+    const CopyTensor &t = p.t[i];
+    const size_t first = (size_t)(blockIdx.x - (i ? p.end[i - 1] : 0u)) * kCopyPiece;
     const int m = blockIdx.y;
     const int d = __ldg(p.dst_slots + m);
     const int s = p.src_slots && t.src ? __ldg(p.src_slots + m) : -1;
@@ -73,7 +75,7 @@ extern "C" int gdn_state_copy(void *const *dst, const void *const *src, const si
     if (nmoves > 0 && !dst_slots) return KKT_ERR_ARG;
     if (!aligned_ptr(dst_slots, 4) || !aligned_ptr(src_slots, 4)) return KKT_ERR_ALIGN;
     CopyParams p = {};
-    size_t most = 0;
+    size_t pieces = 0;  // of a move
     for (int i = 0; i < ntensors; ++i) {
         if ((dst_num_slots > 0 && !dst[i]) || (src && src_num_slots > 0 && !src[i])) return KKT_ERR_ARG;
         // slots of a tensor do not overlap
@@ -84,10 +86,10 @@ extern "C" int gdn_state_copy(void *const *dst, const void *const *src, const si
         p.t[i].bytes = slot_bytes[i];
         p.t[i].dst_stride = dst_stride[i];
         p.t[i].src_stride = src ? src_stride[i] : 0;
-        if (slot_bytes[i] > most) most = slot_bytes[i];
+        pieces += (slot_bytes[i] + kCopyPiece - 1) / kCopyPiece;
+        if (slot_bytes[i] > SIZE_MAX / 2 || pieces > 0x7fffffffu) return KKT_ERR_ARG;
+        p.end[i] = (unsigned)pieces;
     }
-    const size_t pieces = (most + kCopyPiece - 1) / kCopyPiece;
-    if (pieces > 0x7fffffffu) return KKT_ERR_ARG;
     p.dst_num = dst_num_slots;
     p.src_num = src_num_slots;
     const int rc = nmoves > 0 ? status_ptr(&p.status) : KKT_OK;
@@ -96,8 +98,7 @@ extern "C" int gdn_state_copy(void *const *dst, const void *const *src, const si
     for (int m = 0; m < nmoves; m += kMostMoves) {
         p.dst_slots = dst_slots + m;
         p.src_slots = src_slots ? src_slots + m : nullptr;
-        const dim3 grid((unsigned)pieces, (unsigned)(nmoves - m < kMostMoves ? nmoves - m : kMostMoves),
-                        (unsigned)ntensors);
+        const dim3 grid((unsigned)pieces, (unsigned)(nmoves - m < kMostMoves ? nmoves - m : kMostMoves));
         const int e = launch_serialised(state_copy_kernel, grid, kCopyThreads, 0,
                                         reinterpret_cast<cudaStream_t>(stream), p);
         if (e != KKT_OK) return e;
