@@ -158,6 +158,20 @@ __device__ __forceinline__ float2 silu2(float2 x) {
     return mul2(x, make_float2(rcp_approx(1.f + e.x), rcp_approx(1.f + e.y)));
 }
 
+// Asynchronous copies to shared memory, in groups; copy_wait<N> waits for this thread's own copies but
+// for its last N groups.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4_async(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Sum (maximum) over aligned groups of W lanes.
 template <int W>
 __device__ __forceinline__ float lanes_sum(float x) {

@@ -85,17 +85,6 @@ __device__ __forceinline__ void gates(const PrepParams &p, int64_t first, int64_
     }
 }
 
-// Copies of a lane's 8 channels of one row into its own place in shared memory, read back by the same
-// lane, so that a wait for the lane's own copies is all the ordering there is.
-__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Weights and bias of the 8 channels from ch on, in front of the weights zeros where there are fewer
 // than four taps.
 template <typename IO>
@@ -234,6 +223,8 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
     }
     if (t >= end) return;
 
+    // a lane's 8 channels of a row have a place of their own, read back by the lane that copied them, so
+    // that a wait for its own copies is all the ordering there is
     uint8_t *ring = smem + ((threadIdx.x >> 5) * kPrepStages * kPrepBatch * 32 + lane) * (8 * sizeof(IO));
     constexpr int kRowBytes = 32 * 8 * sizeof(IO);
     const int64_t D = p.D;

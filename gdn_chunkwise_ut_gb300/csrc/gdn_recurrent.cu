@@ -9,14 +9,33 @@
 //
 // The columns of S are independent.  A warp owns 16 of them: lane = 4 r + c holds columns 4c .. 4c+3
 // of the rows DK/8 r .. DK/8 (r + 1) - 1, so a row's 16 columns are one 64-byte segment, and the
-// reductions over the rows are in-register sums and three shuffles.  A block is one (sequence, head),
-// its warps the column slabs; no shared memory and no barrier.
+// reductions over the rows are in-register sums and three shuffle steps that halve what they carry.
+// No barrier: a block is four such warps.
+//
+// What bounds it: one token a sequence reads and writes the states and little else, so HBM does.  256
+// sequences of 64 heads, fp32 states: 2.16 GB in 309 us, 105% of the copy rate; 64 x 32 heads 43.3 us
+// (93%); bf16 states 184 us (89%) and 26.8 us (76%), where the memory latency of a warp's whole state
+// in registers weighs more.  One sequence of 16 heads takes 2.8 us, launch and latency.  In longer runs
+// the tokens of a sequence depend on one another: about 0.35 us a token (500 tokens of one sequence:
+// 177 us), or, with the SMs full, the issue slots (33 sequences of 1 to 8 tokens, 16 heads, bf16
+// states: 16.9 us where the bytes take 5.5).  So:
+//   - tokens come through a ring in shared memory, three ahead, by asynchronous copies (without it each
+//     token waited for memory, 24.4 us in that case, and its inputs took registers);
+//   - the state's rows are held in pairs, as k's and q's values lie, for the paired fp32 instructions
+//     (pairs of columns need each of k's values twice, 17.5 us);
+//   - one token a sequence has a kernel of its own, below.
+#include <type_traits>
+
 #include "gdn_layer.cuh"
 
 namespace kkt {
 namespace {
 
 using namespace ptx;
+
+constexpr int kRecWarps = 4;  // of a block: 64 columns
+constexpr int kRecRing = 4;   // tokens in a warp's ring: the one in use and three on their way
+static_assert((kRecRing & (kRecRing - 1)) == 0, "a power of two");
 
 struct RecParams {
     const void *q, *k, *v;
@@ -29,27 +48,165 @@ struct RecParams {
     int *status;
 };
 
-// R consecutive values as fp32 (R a multiple of 8).
-template <int R, typename T>
-__device__ __forceinline__ void load_rows(const T *p, float (&v)[R]) {
+// One token's inputs as a warp has them in shared memory.
+template <typename IO, int DK>
+struct __align__(16) Token {
+    IO k[DK], q[DK], v[16];
+    float beta, g, pad[2];
+};
+
+// From a lane's parts of z = S^T k and y = S^T q (its rows, its C columns) and of k . q to the token's d
+// of the C columns, and, in the lanes with r >= 4, the outputs of the E = C / 4 columns E (r % 4) ...
+// The sums over the eight lanes of a column group halve what a lane carries at each step: lane r ends
+// with z (r < 4) or y of those E columns, whose v the caller gives.
+template <int C>
+__device__ __forceinline__ void token_update(const float (&z)[C], const float (&y)[C], float kq, const float (&v)[C / 4],
+                                             float beta, float a, float scale, int lane, float (&d)[C],
+                                             float (&o)[C / 4]) {
+    constexpr int E = C / 4;
+    const bool hi = lane & 16, mid = lane & 8, lo = lane & 4;
+    float u[C], w[C / 2], sum[E], own[E];
 #pragma unroll
-    for (int i = 0; i < R; i += 8) {
-        float w[8];
-        widen8(raw8(p + i), w);
+    for (int c = 0; c < C; ++c) u[c] = (hi ? y[c] : z[c]) + __shfl_xor_sync(0xffffffffu, hi ? z[c] : y[c], 16);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i + e] = w[e];
+    for (int c = 0; c < C / 2; ++c)
+        w[c] = (mid ? u[c + C / 2] : u[c]) + __shfl_xor_sync(0xffffffffu, mid ? u[c] : u[c + C / 2], 8);
+#pragma unroll
+    for (int c = 0; c < E; ++c)
+        sum[c] = (lo ? w[c + E] : w[c]) + __shfl_xor_sync(0xffffffffu, lo ? w[c] : w[c + E], 4);
+#pragma unroll
+    for (int m = 4; m < 32; m <<= 1) kq += __shfl_xor_sync(0xffffffffu, kq, m);
+    // the lanes with z: d = beta (v - a z); those with y: o = scale (a y + (k . q) d)
+#pragma unroll
+    for (int c = 0; c < E; ++c) own[c] = beta * (v[c] - a * sum[c]);
+#pragma unroll
+    for (int c = 0; c < C; ++c) d[c] = __shfl_sync(0xffffffffu, own[c % E], (c / E) * 4 + (lane & 3));
+#pragma unroll
+    for (int c = 0; c < E; ++c) o[c] = scale * fmaf(kq, __shfl_xor_sync(0xffffffffu, own[c], 16), a * sum[c]);
+}
+
+// 16 bytes of a row of the state, as pairs of columns.
+__device__ __forceinline__ void widen_row(const float4 &r, float2 (&v)[2]) {
+    v[0] = make_float2(r.x, r.y);
+    v[1] = make_float2(r.z, r.w);
+}
+__device__ __forceinline__ void widen_row(const uint4 &r, float2 (&v)[4]) { widen8(Raw8<__nv_bfloat16>{r}, v); }
+// What is computed from a row before this is computed anew behind it, not kept in registers.
+__device__ __forceinline__ void forget(float4 &) {}
+__device__ __forceinline__ void forget(uint4 &r) { asm volatile("" : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)); }
+__device__ __forceinline__ void store_row(float *p, const float2 (&v)[2]) {
+    store4(p, make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+}
+__device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float2 (&v)[4]) { store8(p, v); }
+
+// One token for every sequence: nothing to keep between tokens, so the state stays in registers as it
+// was loaded and is widened in either pass over it.  That lets a lane have 16 bytes of a row for a bf16
+// state too (8 columns, 32 to a warp): as many bytes in flight as for an fp32 state.  Sums in the order
+// of the kernel below, so that decode steps give the bits of one longer call.
+template <typename IO, typename ST, int DK, int DV>
+__global__ void __launch_bounds__(kRecWarps * 32, sizeof(ST) == 4 ? 4 : 3) gdn_recurrent_step_kernel(const RecParams p) {
+    constexpr int R = DK / 8, C = 16 / sizeof(ST), E = C / 4;
+    constexpr int kParts = DV / (4 * C);  // warps of a (sequence, head)
+    using Row = std::conditional_t<sizeof(ST) == 4, float4, uint4>;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t warp = (int64_t)blockIdx.x * kRecWarps + (threadIdx.x >> 5);
+    const int64_t pair = warp / kParts;
+    if (pair >= (int64_t)p.N * p.Hv) return;
+    const int n = (int)(pair / p.Hv), h = (int)(pair % p.Hv);
+    const int lane = threadIdx.x & 31, r = lane >> 2, row0 = r * R;
+    const int col = (int)(warp % kParts) * 4 * C + (lane & 3) * C;  // the lane's first column
+    const int own = col + (r & 3) * E;                             // the first whose sum it ends up with
+    bool ok = true;
+    const int in = slot_of(p.slots, n, p.num_slots, p.status, ok);
+    const int out = p.slots_out ? slot_of(p.slots_out, n, p.num_slots, p.status, ok) : in;
+    const int64_t k_at = ((int64_t)n * p.Hk + h / (p.Hv / p.Hk)) * DK + row0;
+    Raw8<IO> kr[R / 8], qr[R / 8];
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i) {
+        kr[i] = raw8(static_cast<const IO *>(p.k) + k_at + 8 * i);
+        qr[i] = raw8(static_cast<const IO *>(p.q) + k_at + 8 * i);
+    }
+    float v[E];
+#pragma unroll
+    for (int c = 0; c < E; ++c) v[c] = to_f32(static_cast<const IO *>(p.v)[pair * DV + own + c]);
+    const float beta = __ldg(p.beta + pair);
+    const float a = p.g ? expf(__ldg(p.g + pair)) : 1.f;
+    if (!ok) return;
+    const int64_t off = ((int64_t)h * DK + row0) * DV + col, slot_size = (int64_t)p.Hv * DK * DV;
+    Row S[R] = {};
+    if (in >= 0) {
+        const ST *from = static_cast<const ST *>(p.state) + in * slot_size + off;
+#pragma unroll
+        for (int i = 0; i < R; ++i) S[i] = *reinterpret_cast<const Row *>(from + i * DV);
+    }
+    // z and y of the even and of the odd rows
+    float2 z[2][C / 2] = {}, y[2][C / 2] = {}, kq = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i) {
+        float2 k2[4], q2[4];
+        widen8(kr[i], k2);
+        widen8(qr[i], q2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float kv = e & 1 ? k2[e / 2].y : k2[e / 2].x, qv = e & 1 ? q2[e / 2].y : q2[e / 2].x;
+            float2 s[C / 2];
+            widen_row(S[8 * i + e], s);
+#pragma unroll
+            for (int c = 0; c < C / 2; ++c) {
+                z[e & 1][c] = fma2(s[c], make_float2(kv, kv), z[e & 1][c]);
+                y[e & 1][c] = fma2(s[c], make_float2(qv, qv), y[e & 1][c]);
+            }
+            if (e & 1) kq = fma2(k2[e / 2], q2[e / 2], kq);
+        }
+    }
+    float zs[C], ys[C], d[C], o[E];
+#pragma unroll
+    for (int c = 0; c < C / 2; ++c) {
+        zs[2 * c] = z[0][c].x + z[1][c].x;
+        zs[2 * c + 1] = z[0][c].y + z[1][c].y;
+        ys[2 * c] = y[0][c].x + y[1][c].x;
+        ys[2 * c + 1] = y[0][c].y + y[1][c].y;
+    }
+    token_update<C>(zs, ys, kq.x + kq.y, v, beta, a, p.scale, lane, d, o);
+    if (r & 4) {
+#pragma unroll
+        for (int c = 0; c < E; ++c) static_cast<IO *>(p.o)[pair * DV + own + c] = from_f32<IO>(o[c]);
+    }
+    if (out < 0) return;
+#pragma unroll
+    for (int i = 0; i < R; ++i) forget(S[i]);
+    ST *to = static_cast<ST *>(p.state) + out * slot_size + off;
+    const float2 a2 = make_float2(a, a);
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i) {
+        float2 k2[4];
+        widen8(kr[i], k2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float kv = e & 1 ? k2[e / 2].y : k2[e / 2].x;
+            float2 s[C / 2];
+            widen_row(S[8 * i + e], s);
+#pragma unroll
+            for (int c = 0; c < C / 2; ++c)
+                s[c] = fma2(make_float2(kv, kv), make_float2(d[2 * c], d[2 * c + 1]), mul2(a2, s[c]));
+            store_row(to + (8 * i + e) * DV, s);
+        }
     }
 }
 
 template <typename IO, typename ST, int DK, int DV>
-__global__ void __launch_bounds__(2 * DV) gdn_recurrent_kernel(const RecParams p) {
+__global__ void __launch_bounds__(kRecWarps * 32) gdn_recurrent_kernel(const RecParams p) {
     constexpr int R = DK / 8;
+    constexpr int kSlabs = DV / 16 / kRecWarps;  // blocks of a (sequence, head)
     griddep_launch_dependents();
     griddep_wait();
-    const int n = blockIdx.x / p.Hv, h = blockIdx.x % p.Hv;
+    const int pair = blockIdx.x / kSlabs;
+    const int n = pair / p.Hv, h = pair % p.Hv;
     const int lane = threadIdx.x & 31;
-    const int row0 = (lane >> 2) * R;
-    const int col = (threadIdx.x >> 5) * 16 + (lane & 3) * 4;
+    const int r = lane >> 2;
+    const int row0 = r * R;
+    const int col = ((blockIdx.x % kSlabs) * kRecWarps + (threadIdx.x >> 5)) * 16 + (lane & 3) * 4;
     Span s = seq_span(p.cu, n, p.N, p.T, p.ntok, p.status);
     const int in = slot_of(p.slots, n, p.num_slots, p.status, s.ok);
     const int out = p.slots_out ? slot_of(p.slots_out, n, p.num_slots, p.status, s.ok) : in;
@@ -57,71 +214,126 @@ __global__ void __launch_bounds__(2 * DV) gdn_recurrent_kernel(const RecParams p
     const int64_t off = ((int64_t)h * DK + row0) * DV + col;
     const int64_t slot_size = (int64_t)p.Hv * DK * DV;
 
-    float S[R][4];
-    const ST *src = static_cast<const ST *>(p.state) + in * slot_size + off;
+    __shared__ Token<IO, DK> ring_all[kRecWarps][kRecRing];
+    Token<IO, DK> *ring = ring_all[threadIdx.x >> 5];
+    const int col0 = col - (lane & 3) * 4;  // the warp's first column
+    const int64_t k_step = (int64_t)p.Hk * DK, v_step = (int64_t)p.Hv * DV;
+    const int64_t k_at = s.a * k_step + (h / (p.Hv / p.Hk)) * DK;
+    IO *o = static_cast<IO *>(p.o) + s.a * v_step + (int64_t)h * DV + col + (r & 3);
+    const int count = (int)(s.b - s.a);
+    // The warp's lanes share the copies of a token: its k and q in pieces of 16 bytes, kShare to a lane,
+    // then v, beta and g by a lane for each piece of them.  Sources move on by a token with each fetch.
+    constexpr int V = 16 / sizeof(IO), KC = DK / V, VC = 16 / V, kShare = (2 * KC + 31) / 32;
+    const IO *src[kShare];
+    int dst[kShare];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const float4 x = in >= 0 ? load4(src + i * DV) : make_float4(0.f, 0.f, 0.f, 0.f);
-        S[i][0] = x.x; S[i][1] = x.y; S[i][2] = x.z; S[i][3] = x.w;
+    for (int i = 0; i < kShare; ++i) {
+        const int e = i * 32 + lane;  // piece e of k, then of q
+        src[i] = static_cast<const IO *>(e < KC ? p.k : p.q) + k_at + (e < KC ? e : e - KC) * V;
+        dst[i] = e * V;  // q lies behind k
     }
-    const int hk = h / (p.Hv / p.Hk);
-    const IO *q = static_cast<const IO *>(p.q) + hk * DK + row0;
-    const IO *k = static_cast<const IO *>(p.k) + hk * DK + row0;
-    for (int64_t t = s.a; t < s.b; ++t) {
-        float kv[R], qv[R];
-        load_rows(k + t * p.Hk * DK, kv);
-        load_rows(q + t * p.Hk * DK, qv);
-        const int64_t tv = t * p.Hv + h;
-        const float4 v = load4(static_cast<const IO *>(p.v) + tv * DV + col);
-        const float beta = __ldg(p.beta + tv);
-        const float a = p.g ? expf(__ldg(p.g + tv)) : 1.f;
-        float z[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f}, kq = 0.f;
+    const IO *vsrc = static_cast<const IO *>(p.v) + s.a * v_step + (int64_t)h * DV + col0 + lane * V;
+    const float *gsrc = lane == VC ? p.beta : lane == VC + 1 ? p.g : nullptr;
+    if (gsrc) gsrc += s.a * p.Hv + h;
+    // token t into its place of the ring, if there is one
+    auto fetch = [&](int t) {
+        if (t < count) {
+            Token<IO, DK> &x = ring[t & (kRecRing - 1)];
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            kq = fmaf(kv[i], qv[i], kq);
+            for (int i = 0; i < kShare; ++i) {
+                if (2 * KC >= 32 || lane < 2 * KC) copy16_async(x.k + dst[i], src[i]);
+                src[i] += k_step;
+            }
+            if (lane < VC) copy16_async(x.v + lane * V, vsrc);
+            if (gsrc) {
+                copy4_async(lane == VC ? &x.beta : &x.g, gsrc);
+                gsrc += p.Hv;
+            }
+            vsrc += v_step;
+        }
+        copy_commit();
+    };
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                z[c] = fmaf(S[i][c], kv[i], z[c]);
-                y[c] = fmaf(S[i][c], qv[i], y[c]);
+    for (int t = 0; t < kRecRing - 1; ++t) fetch(t);
+
+    // S by pairs of rows: S[i][c] has rows 2 i and 2 i + 1 of column c, as a pair of k's values has them
+    float2 S[R / 2][4];
+    const ST *from = static_cast<const ST *>(p.state) + in * slot_size + off;
+#pragma unroll
+    for (int i = 0; i < R / 2; ++i) {
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 x = in >= 0 ? load4(from + 2 * i * DV) : zero, y = in >= 0 ? load4(from + (2 * i + 1) * DV) : zero;
+        S[i][0] = make_float2(x.x, y.x); S[i][1] = make_float2(x.y, y.y);
+        S[i][2] = make_float2(x.z, y.z); S[i][3] = make_float2(x.w, y.w);
+    }
+    for (int t = 0; t < count; ++t) {
+        copy_wait<kRecRing - 2>();
+        __syncwarp();  // every lane's copies of token t are there, and every lane is done with token t - 1
+        fetch(t + kRecRing - 1);
+        const Token<IO, DK> &x = ring[t & (kRecRing - 1)];
+        const float a = p.g ? expf(x.g) : 1.f;
+        // z = S^T k, y = S^T q and k . q over this lane's rows
+        float2 z2[4] = {}, y2[4] = {}, kq2 = make_float2(0.f, 0.f), kv[R / 2];
+#pragma unroll
+        for (int i = 0; i < R / 8; ++i) {
+            float2 k2[4], q2[4];
+            widen8(raw8(x.k + row0 + 8 * i), k2);
+            widen8(raw8(x.q + row0 + 8 * i), q2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = 4 * i + e;
+                kv[j] = k2[e];
+                kq2 = fma2(k2[e], q2[e], kq2);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    z2[c] = fma2(S[j][c], k2[e], z2[c]);
+                    y2[c] = fma2(S[j][c], q2[e], y2[c]);
+                }
             }
         }
-#pragma unroll
-        for (int m = 4; m < 32; m <<= 1) {
-            kq += __shfl_xor_sync(0xffffffffu, kq, m);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                z[c] += __shfl_xor_sync(0xffffffffu, z[c], m);
-                y[c] += __shfl_xor_sync(0xffffffffu, y[c], m);
-            }
-        }
-        const float vv[4] = {v.x, v.y, v.z, v.w};
-        float d[4], ov[4];
+        float z[4], y[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            d[c] = beta * (vv[c] - a * z[c]);
-            ov[c] = p.scale * fmaf(kq, d[c], a * y[c]);
+            z[c] = z2[c].x + z2[c].y;
+            y[c] = y2[c].x + y2[c].y;
         }
+        const float vv[1] = {to_f32(x.v[(lane & 3) * 4 + (r & 3)])};
+        float d[4], ov[1];
+        token_update<4>(z, y, kq2.x + kq2.y, vv, x.beta, a, p.scale, lane, d, ov);
+        if (r & 4) *o = from_f32<IO>(ov[0]);
+        o += v_step;
+        const float2 a2 = make_float2(a, a);
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+        for (int j = 0; j < R / 2; ++j)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) S[i][c] = fmaf(kv[i], d[c], a * S[i][c]);
-        if (lane < 4) store4(static_cast<IO *>(p.o) + tv * DV + col, make_float4(ov[0], ov[1], ov[2], ov[3]));
+            for (int c = 0; c < 4; ++c) S[j][c] = fma2(kv[j], make_float2(d[c], d[c]), mul2(a2, S[j][c]));
     }
-    if (out >= 0 && (out != in || s.b > s.a)) {
-        ST *dst = static_cast<ST *>(p.state) + out * slot_size + off;
+    if (out >= 0 && (out != in || count > 0)) {
+        ST *to = static_cast<ST *>(p.state) + out * slot_size + off;
 #pragma unroll
-        for (int i = 0; i < R; ++i) store4(dst + i * DV, make_float4(S[i][0], S[i][1], S[i][2], S[i][3]));
+        for (int i = 0; i < R / 2; ++i) {
+            store4(to + 2 * i * DV, make_float4(S[i][0].x, S[i][1].x, S[i][2].x, S[i][3].x));
+            store4(to + (2 * i + 1) * DV, make_float4(S[i][0].y, S[i][1].y, S[i][2].y, S[i][3].y));
+        }
     }
+}
+
+template <typename IO, typename ST, int DK, int DV>
+int launch(const RecParams &p, cudaStream_t st) {
+    const int64_t pairs = (int64_t)p.N * p.Hv;
+    if (!p.cu && p.T == 1) {
+        constexpr int kParts = DV * (int)sizeof(ST) / 64;
+        const dim3 grid((unsigned)((pairs * kParts + kRecWarps - 1) / kRecWarps));
+        return launch_serialised(gdn_recurrent_step_kernel<IO, ST, DK, DV>, grid, kRecWarps * 32, 0, st, p);
+    }
+    const dim3 grid((unsigned)(pairs * (DV / 16 / kRecWarps)));
+    return launch_serialised(gdn_recurrent_kernel<IO, ST, DK, DV>, grid, kRecWarps * 32, 0, st, p);
 }
 
 template <typename IO, typename ST>
 int launch(const RecParams &p, int dk, int dv, cudaStream_t st) {
-    const dim3 grid((unsigned)(p.N * p.Hv));
-    if (dk == 128)
-        return dv == 128 ? launch_serialised(gdn_recurrent_kernel<IO, ST, 128, 128>, grid, 256, 0, st, p)
-                         : launch_serialised(gdn_recurrent_kernel<IO, ST, 128, 64>, grid, 128, 0, st, p);
-    return dv == 128 ? launch_serialised(gdn_recurrent_kernel<IO, ST, 64, 128>, grid, 256, 0, st, p)
-                     : launch_serialised(gdn_recurrent_kernel<IO, ST, 64, 64>, grid, 128, 0, st, p);
+    if (dk == 128) return dv == 128 ? launch<IO, ST, 128, 128>(p, st) : launch<IO, ST, 128, 64>(p, st);
+    return dv == 128 ? launch<IO, ST, 64, 128>(p, st) : launch<IO, ST, 64, 64>(p, st);
 }
 
 }  // namespace
@@ -137,7 +349,7 @@ extern "C" int gdn_recurrent_fwd(const void *q, const void *k, const void *v, co
         return KKT_ERR_ARG;
     if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return KKT_ERR_UNSUPPORTED;
     const int64_t ntok = cu_seqlens ? (int64_t)T : (int64_t)N * T;
-    if (ntok > 0x7fffffffLL || (int64_t)N * Hv > 0x7fffffffLL) return KKT_ERR_ARG;
+    if (ntok > 0x7fffffffLL || (int64_t)N * Hv * (dv / 16 / kRecWarps) > 0x7fffffffLL) return KKT_ERR_ARG;
     if (ntok > 0 && (!q || !k || !v || !beta || !o)) return KKT_ERR_ARG;
     if (num_slots > 0 && !state) return KKT_ERR_ARG;
     if (!slots && N > num_slots) return KKT_ERR_ARG;
