@@ -3,8 +3,9 @@
 // these calls for every layer and token with kernels of a few microseconds, so the marshalling is
 // native: through ctypes a call took 16 to 45 us of the host's time, see layer.py.
 //
-// A function returns its outputs, or the kkt_status of a refused call as an int; what the arguments
-// themselves show to be wrong raises ValueError.
+// A function returns its outputs, or as an int the kkt_status of a refused call, or, negated, what a
+// checked call found in the device's status word; what the arguments themselves show to be wrong raises
+// ValueError.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -15,6 +16,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
+#include <cstdlib>
+#include <cstring>
 #include <string>
 #include <vector>
 
@@ -127,6 +131,22 @@ PyObject *guarded(F f) {
     END_HANDLE_TH_ERRORS
 }
 
+// The end of a call: its status as an int where there is something to say, else nullptr.  In the checked
+// mode (`check` true, or None and KKT_CHECK=1 in the environment) the stream is waited for and the
+// device's status word read and cleared.
+PyObject *trouble(int rc, PyObject *check, CUstream_st *stream) {
+    if (rc != KKT_OK) return PyLong_FromLong(rc);
+    bool checked = check == Py_True;
+    if (check == Py_None) {
+        const char *env = std::getenv("KKT_CHECK");
+        checked = env && std::strcmp(env, "1") == 0;
+    } else if (!checked) {
+        checked = PyObject_IsTrue(check) == 1;
+    }
+    if (checked && (rc = kkt_device_status(stream)) != KKT_OK) return PyLong_FromLong(-rc);
+    return nullptr;
+}
+
 bool arity(Py_ssize_t n, Py_ssize_t want) {
     if (n == want) return true;
     PyErr_Format(PyExc_TypeError, "%zd arguments expected, %zd given", want, n);
@@ -146,9 +166,9 @@ PyObject *wrap_all(const T &...t) {
     return tuple;
 }
 
-// q, k, v, beta, state, g, slots, slots_out, cu_seqlens, scale, o
+// q, k, v, beta, state, g, slots, slots_out, cu_seqlens, scale, o, check
 PyObject *recurrent(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arity(n, 11)) return nullptr;
+    if (!arity(n, 12)) return nullptr;
     return guarded([&]() -> PyObject * {
         const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &beta = tensor(a[3], "beta"),
                      &state = tensor(a[4], "state");
@@ -173,21 +193,22 @@ PyObject *recurrent(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (slots_out.defined()) check(slots_out, "slots_out", at::kInt, {N}, dev);
         const double scale = a[9] == Py_None ? 1.0 / std::sqrt((double)dk) : number(a[9], "scale");
         const c10::cuda::CUDAGuard guard(dev);
+        CUstream_st *stream = stream_on(dev);
         if (o.defined()) check(o, "o", dt, v.sizes(), dev);
         else o = empty(v.sizes(), dt, dev);
         const int rc = gdn_recurrent_fwd(raw(q), raw(k), raw(v), ptr<float>(beta), ptr<float>(g), ptr<int32_t>(cu), N,
                                          small(T, "T"), small(Hk, "Hk"), small(Hv, "Hv"), small(dk, "dk"),
                                          small(dv, "dv"), (float)scale, io, raw(state), st, small(P, "P"),
-                                         ptr<int32_t>(slots), ptr<int32_t>(slots_out), raw(o), stream_on(dev));
-        if (rc != KKT_OK) return PyLong_FromLong(rc);
+                                         ptr<int32_t>(slots), ptr<int32_t>(slots_out), raw(o), stream);
+        if (PyObject *said = trouble(rc, a[11], stream)) return said;
         if (a[10] != Py_None) return Py_NewRef(a[10]);
         return wrap(o);
     });
 }
 
-// x, weight, a, b, A_log, dt_bias, conv_state, Hk, Hv, dk, dv, bias, slots, cu_seqlens, expand, eps
+// x, weight, a, b, A_log, dt_bias, conv_state, Hk, Hv, dk, dv, bias, slots, cu_seqlens, expand, eps, check
 PyObject *prep(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arity(n, 16)) return nullptr;
+    if (!arity(n, 17)) return nullptr;
     return guarded([&]() -> PyObject * {
         const Tensor &x = tensor(a[0], "x"), &weight = tensor(a[1], "weight"), &ga = tensor(a[2], "a"),
                      &gb = tensor(a[3], "b"), &A_log = tensor(a[4], "A_log"), &dt_bias = tensor(a[5], "dt_bias"),
@@ -217,6 +238,7 @@ PyObject *prep(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int N = sequences(cu, B, dev);
         if (slots.defined()) check(slots, "slots", at::kInt, {N}, dev);
         const c10::cuda::CUDAGuard guard(dev);
+        CUstream_st *stream = stream_on(dev);
         const int64_t Hq = expand ? Hv : Hk;
         const Tensor q = empty({B, T, Hq, dk}, dt, dev), k = empty({B, T, Hq, dk}, dt, dev),
                      v = empty({B, T, Hv, dv}, dt, dev), g = empty({B, T, Hv}, at::kFloat, dev),
@@ -225,8 +247,8 @@ PyObject *prep(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                     ptr<float>(dt_bias), ptr<int32_t>(cu), N, small(T, "T"), Hk, Hv, dk, dv,
                                     small(taps, "taps"), (float)eps, expand, io, raw(conv), small(P, "P"),
                                     ptr<int32_t>(slots), raw(q), raw(k), raw(v), ptr<float>(g), ptr<float>(beta),
-                                    stream_on(dev));
-        if (rc != KKT_OK) return PyLong_FromLong(rc);
+                                    stream);
+        if (PyObject *said = trouble(rc, a[16], stream)) return said;
         return wrap_all(q, k, v, g, beta);
     });
 }
@@ -245,9 +267,9 @@ ScalarType out_type(PyObject *o, const Tensor &x, int &code) {
     return t;
 }
 
-// x, weight, residual, eps, out_dtype, group, residual_out
+// x, weight, residual, eps, out_dtype, group, residual_out, check
 PyObject *add_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arity(n, 7)) return nullptr;
+    if (!arity(n, 8)) return nullptr;
     return guarded([&]() -> PyObject * {
         const Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "weight");
         const Tensor r = optional(a[2], "residual");
@@ -268,6 +290,7 @@ PyObject *add_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (a[5] != Py_None && group != 128) refuse("group must be 128 or None, got " + std::to_string(group));
         const double eps = number(a[3], "eps");
         const c10::cuda::CUDAGuard guard(dev);
+        CUstream_st *stream = stream_on(dev);
         if (r.defined() && !r_out.defined()) r_out = empty(x.sizes(), dt, dev);
         const Tensor y = empty(x.sizes(), out, dev);
         Tensor scales;
@@ -278,8 +301,8 @@ PyObject *add_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
             scales = empty(shape, at::kFloat, dev);
         }
         const int rc = add_rms_norm_fwd(raw(x), raw(r), raw(w), dim ? x.numel() / dim : 0, small(dim, "dim"), (float)eps,
-                                        io, code, group, raw(y), ptr<float>(scales), raw(r_out), stream_on(dev));
-        if (rc != KKT_OK) return PyLong_FromLong(rc);
+                                        io, code, group, raw(y), ptr<float>(scales), raw(r_out), stream);
+        if (PyObject *said = trouble(rc, a[7], stream)) return said;
         if (a[6] != Py_None) {
             PyObject *tuple = wrap_all(y, scales, Tensor());
             PyTuple_SetItem(tuple, 2, Py_NewRef(a[6]));
@@ -289,9 +312,9 @@ PyObject *add_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// x, z, weight, eps, out_dtype
+// x, z, weight, eps, out_dtype, check
 PyObject *gated_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arity(n, 5)) return nullptr;
+    if (!arity(n, 6)) return nullptr;
     return guarded([&]() -> PyObject * {
         const Tensor &x = tensor(a[0], "x"), &z = tensor(a[1], "z"), &w = tensor(a[2], "weight");
         if (x.dim() < 1) refuse("expected x [..., d]");
@@ -306,12 +329,13 @@ PyObject *gated_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const ScalarType out = out_type(a[4], x, code);
         const double eps = number(a[3], "eps");
         const c10::cuda::CUDAGuard guard(dev);
+        CUstream_st *stream = stream_on(dev);
         const Tensor y = empty(x.sizes(), out, dev);
         Tensor scales;
         if (code == GDN_OUT_E4M3) scales = empty(x.sizes().slice(0, x.dim() - 1), at::kFloat, dev);
         const int rc = gated_rms_norm_fwd(raw(x), raw(z), raw(w), dim ? x.numel() / dim : 0, small(dim, "dim"),
-                                          (float)eps, io, code, raw(y), ptr<float>(scales), stream_on(dev));
-        if (rc != KKT_OK) return PyLong_FromLong(rc);
+                                          (float)eps, io, code, raw(y), ptr<float>(scales), stream);
+        if (PyObject *said = trouble(rc, a[5], stream)) return said;
         return wrap_all(y, scales);
     });
 }
@@ -366,9 +390,9 @@ Side side(PyObject *o, const char *name) {
     return s;
 }
 
-// dst, dst_slots, src, src_slots
+// dst, dst_slots, src, src_slots, check
 PyObject *state_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arity(n, 4)) return nullptr;
+    if (!arity(n, 5)) return nullptr;
     return guarded([&]() -> PyObject * {
         const Side dst = side(a[0], "dst");
         const c10::Device dev = dst.t[0].device();
@@ -390,13 +414,16 @@ PyObject *state_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         const Side &src = copies && a[2] != a[0] ? other : dst;
         if (copies) check(src_slots, "src_slots", at::kInt, dst_slots.sizes(), dev);
-        if (dst.slots == 0 || dst_slots.numel() == 0) return PyLong_FromLong(KKT_OK);
+        if (dst.slots == 0 || dst_slots.numel() == 0) Py_RETURN_NONE;
         const c10::cuda::CUDAGuard guard(dev);
-        return PyLong_FromLong(gdn_state_copy(
+        CUstream_st *stream = stream_on(dev);
+        const int rc = gdn_state_copy(
             dst.ptrs.data(), copies ? const_cast<const void *const *>(src.ptrs.data()) : nullptr, dst.bytes.data(),
             dst.stride.data(), copies ? src.stride.data() : nullptr, (int)dst.t.size(), ptr<int32_t>(dst_slots),
             ptr<int32_t>(src_slots), small(dst_slots.numel(), "dst_slots"), small(dst.slots, "P"),
-            copies ? small(src.slots, "P") : 0, stream_on(dev)));
+            copies ? small(src.slots, "P") : 0, stream);
+        if (PyObject *said = trouble(rc, a[4], stream)) return said;
+        Py_RETURN_NONE;
     });
 }
 

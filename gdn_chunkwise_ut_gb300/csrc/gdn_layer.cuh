@@ -125,6 +125,12 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
         : "=l"(reinterpret_cast<uint64_t &>(d))
         : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
     return d;
+}__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
 }
 
 // Eight values as four pairs.
@@ -155,7 +161,8 @@ __device__ __forceinline__ float2 silu2(float2 x) {
     float2 e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-    return mul2(x, make_float2(rcp_approx(1.f + e.x), rcp_approx(1.f + e.y)));
+    e = make_float2(1.f + e.x, 1.f + e.y);
+    return mul2(x, make_float2(rcp_approx(e.x), rcp_approx(e.y)));
 }
 
 // Asynchronous copies to shared memory, in groups; copy_wait<N> waits for this thread's own copies but

@@ -10,24 +10,15 @@ step, and a call marshalled in Python took 16 to 45 us of the host's time.
 """
 from __future__ import annotations
 
-import os
-
 import torch
 
 from . import _lib
-from .api import device_status
 
 
-def _done(result, what, check):
+def _done(result, what):
     """The call's result; KktError for a refused call, or, when checked, for what the device recorded."""
-    if result.__class__ is int and result != _lib.KKT_OK:
-        raise _lib.KktError(result, what)
-    if check is None:
-        check = os.environ.get("KKT_CHECK", "0") == "1"
-    if check:
-        st = device_status()
-        if st != _lib.KKT_OK:
-            raise _lib.KktError(st, f"{what} (device)")
+    if result.__class__ is int:
+        raise _lib.KktError(result, what) if result > 0 else _lib.KktError(-result, f"{what} (device)")
     return result
 
 
@@ -50,8 +41,9 @@ def gdn_recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: t
         with torch.cuda.stream(stream):
             return gdn_recurrent_fwd(q, k, v, beta, state, g=g, slots=slots, slots_out=slots_out,
                                      cu_seqlens=cu_seqlens, scale=scale, o=o, check=check)
-    result = _lib.binding().recurrent(q, k, v, beta, state, g, slots, slots_out, cu_seqlens, scale, o)
-    return _done(result, "gdn_recurrent_fwd", check)
+    result = _lib.binding().recurrent(q, k, v, beta, state, g, slots, slots_out, cu_seqlens, scale, o,
+                                       check)
+    return _done(result, "gdn_recurrent_fwd")
 
 
 def gdn_prep_fwd(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: torch.Tensor, A_log: torch.Tensor,
@@ -77,8 +69,8 @@ def gdn_prep_fwd(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: torc
             return gdn_prep_fwd(x, weight, a, b, A_log, dt_bias, conv_state, Hk=Hk, Hv=Hv, dk=dk, dv=dv, bias=bias,
                                 slots=slots, cu_seqlens=cu_seqlens, expand=expand, eps=eps, check=check)
     result = _lib.binding().prep(x, weight, a, b, A_log, dt_bias, conv_state, Hk, Hv, dk, dv, bias, slots,
-                                  cu_seqlens, expand, eps)
-    return _done(result, "gdn_prep_fwd", check)
+                                  cu_seqlens, expand, eps, check)
+    return _done(result, "gdn_prep_fwd")
 
 
 def add_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, *, eps: float = 1e-6,
@@ -96,8 +88,8 @@ def add_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
         with torch.cuda.stream(stream):
             return add_rms_norm_fwd(x, weight, residual, eps=eps, out_dtype=out_dtype, group=group,
                                     residual_out=residual_out, check=check)
-    result = _lib.binding().add_norm(x, weight, residual, eps, out_dtype, group, residual_out)
-    return _done(result, "add_rms_norm_fwd", check)
+    result = _lib.binding().add_norm(x, weight, residual, eps, out_dtype, group, residual_out, check)
+    return _done(result, "add_rms_norm_fwd")
 
 
 def gated_rms_norm_fwd(x: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, out_dtype=None,
@@ -111,8 +103,8 @@ def gated_rms_norm_fwd(x: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *
     if stream is not None:
         with torch.cuda.stream(stream):
             return gated_rms_norm_fwd(x, z, weight, eps=eps, out_dtype=out_dtype, check=check)
-    result = _lib.binding().gated_norm(x, z, weight, eps, out_dtype)
-    return _done(result, "gated_rms_norm_fwd", check)
+    result = _lib.binding().gated_norm(x, z, weight, eps, out_dtype, check)
+    return _done(result, "gated_rms_norm_fwd")
 
 
 def gdn_state_copy(dst, dst_slots: torch.Tensor, src=None, src_slots: torch.Tensor | None = None, *, stream=None,
@@ -129,5 +121,5 @@ def gdn_state_copy(dst, dst_slots: torch.Tensor, src=None, src_slots: torch.Tens
     if stream is not None:
         with torch.cuda.stream(stream):
             return gdn_state_copy(dst, dst_slots, src, src_slots, check=check)
-    result = _lib.binding().state_copy(dst, dst_slots, src, src_slots)
-    _done(result, "gdn_state_copy", check)
+    result = _lib.binding().state_copy(dst, dst_slots, src, src_slots, check)
+    _done(result, "gdn_state_copy")
