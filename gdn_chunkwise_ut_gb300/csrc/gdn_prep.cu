@@ -19,9 +19,7 @@
 //
 // The convolution's state is read, and its successor written, by the warp that has the sequence's
 // first token, whichever run holds the last one: the same thread reads and writes each element, so
-// updating the pool in place needs no order between warps.  For that, the tokens whose window reaches
-// into the state belong to that warp too: a run goes on over them past its end, and the next one
-// leaves them out.
+// updating the pool in place needs no order between warps.
 #include "gdn_layer.cuh"
 
 namespace kkt {
@@ -47,29 +45,40 @@ struct PrepParams {
     int *status;
 };
 
-// The sequence of token t: the last one that starts at or before it (empty ones before it are passed
-// over).  False, with the error recorded, where cu_seqlens is malformed there.
-__device__ __forceinline__ bool seq_of_token(const PrepParams &p, int t, int &n, int &a, int &b) {
+// The tokens of a work id: `count` of sequence n from token t0 on, a run that restarts at every sequence.
+// Packed sequences: sequence s owns the ids from floor(start(s) / run) + s on, at least as many as it has
+// runs (as kkt_internal.cuh numbers chunks); the ids left over are idle.  False for those, and, with the
+// error recorded, where cu_seqlens is malformed or the sequence's slot is past the pool's end.
+struct Run {
+    int n, a, b, t0, count, slot;
+};
+__device__ __forceinline__ bool run_of(const PrepParams &p, int id, Run &r) {
+    bool ok = true;
     if (!p.cu) {
-        n = t / p.T;
-        a = n * p.T;
-        b = a + p.T;
-        return true;
+        const int per = (p.T + p.run - 1) / p.run;
+        r.n = id / per;
+        r.a = r.n * p.T;
+        r.b = r.a + p.T;
+        r.t0 = r.a + (id - r.n * per) * p.run;
+    } else {
+        int lo = 0, hi = p.N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((int64_t)(__ldg(p.cu + mid) / p.run) + mid <= id) lo = mid; else hi = mid - 1;
+        }
+        const Span s = seq_span(p.cu, lo, p.N, p.T, p.ntok, p.status);
+        if (!s.ok) return false;
+        r.n = lo;
+        r.a = (int)s.a;
+        r.b = (int)s.b;
+        const int64_t t0 = s.a + (int64_t)(id - lo - r.a / p.run) * p.run;
+        if (t0 < s.a) record_error(p.status, KKT_ERR_SEQLENS);
+        if (t0 < s.a || t0 >= s.b) return false;
+        r.t0 = (int)t0;
     }
-    int lo = 0, hi = p.N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(p.cu + mid) <= t) lo = mid; else hi = mid - 1;
-    }
-    n = lo;
-    const Span s = seq_span(p.cu, n, p.N, p.T, p.ntok, p.status);
-    a = (int)s.a;
-    b = (int)s.b;
-    if (s.ok && (t < a || t >= b)) {
-        record_error(p.status, KKT_ERR_SEQLENS);
-        return false;
-    }
-    return s.ok;
+    r.slot = slot_of(p.slots, r.n, p.num_slots, p.status, ok);
+    r.count = r.b - r.t0 < p.run ? r.b - r.t0 : p.run;
+    return ok;
 }
 
 // beta = sigmoid(b) and g = -e^{A_log} softplus(a + dt_bias) of `count` consecutive (token, head) pairs.
@@ -147,9 +156,9 @@ __device__ __forceinline__ HeadOut<IO> head_out(const PrepParams &p, int ch) {
     return h;
 }
 
-// SiLU, the norm where the head has one, and the stores, of B tokens side by side.
+// SiLU, the norm where the head has one, and the stores of the first `store`, of B tokens side by side.
 template <typename IO, int DH, int B>
-__device__ __forceinline__ void finish(const PrepParams &p, const HeadOut<IO> &h, float2 (&y)[B][4], IO *o, bool store) {
+__device__ __forceinline__ void finish(const PrepParams &p, const HeadOut<IO> &h, float2 (&y)[B][4], IO *o, int store) {
 #pragma unroll
     for (int i = 0; i < B; ++i)
 #pragma unroll
@@ -174,13 +183,12 @@ __device__ __forceinline__ void finish(const PrepParams &p, const HeadOut<IO> &h
             for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], make_float2(r, r));
         }
     }
-    if (store) {
 #pragma unroll
-        for (int i = 0; i < B; ++i) store8(o + i * h.stride, y[i]);
-        for (int c = 1; c < h.copies; ++c)
-#pragma unroll
-            for (int i = 0; i < B; ++i) store8(o + i * h.stride + c * DH, y[i]);
-    }
+    for (int i = 0; i < B; ++i)
+        if (i < store) {
+            store8(o + i * h.stride, y[i]);
+            for (int c = 1; c < h.copies; ++c) store8(o + i * h.stride + c * DH, y[i]);
+        }
 }
 
 template <typename IO, int DH>
@@ -190,139 +198,90 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int slab = blockIdx.y * kPrepWarps + (threadIdx.x >> 5);
-    // tokens are counted in 32 bits (there are fewer than 2^31)
-    const int ntok = (int)p.ntok;
-    const int t0 = (int)blockIdx.x * p.run;
-    const int t1 = ntok - t0 < p.run ? ntok : t0 + p.run;
     if (slab > p.slabs) return;
+    if (slab == p.slabs && blockIdx.x == 0 && p.cu)
+        for (int n = lane; n < p.N; n += 32) check_sequence(p.cu, n, p.N, p.ntok, p.status);
+    Run r;
+    if (!run_of(p, blockIdx.x, r)) return;
     if (slab == p.slabs) {
-        gates<IO>(p, (int64_t)t0 * p.Hv, (int64_t)(t1 - t0) * p.Hv, lane);
-        if (blockIdx.x == 0 && p.cu)
-            for (int n = lane; n < p.N; n += 32) check_sequence(p.cu, n, p.N, p.ntok, p.status);
+        gates<IO>(p, (int64_t)r.t0 * p.Hv, (int64_t)r.count * p.Hv, lane);
         return;
     }
     const int ch = slab * kSlab + lane * 8;
     const bool live = ch < p.D;  // the last slab may be short
     const int chc = live ? ch : 0;
     const int keep = p.taps - 1;
-    const IO *x = static_cast<const IO *>(p.x) + chc;
-
-    // this warp's tokens [t, end)
-    int n = 0, a = 0, b = 0;
-    int t = t0, end = t1;
-    bool ok = seq_of_token(p, t0, n, a, b);
-    if (keep > 1) {
-        if (ok && t0 > a && t0 - a < keep) t = b - a > keep ? a + keep : b;
-        int la = a, lb = b;  // the last token's sequence
-        bool lok = ok;
-        if (!ok || b < t1) {
-            int ln;
-            lok = seq_of_token(p, t1 - 1, ln, la, lb);
-        }
-        if (lok && la >= t0 && lb > t1 && t1 - la < keep) end = lb - la > keep ? la + keep : lb;
-    }
-    if (t >= end) return;
+    const int64_t D = p.D;
+    const IO *x = static_cast<const IO *>(p.x) + r.t0 * D + chc;  // the run's first row
 
     // a lane's 8 channels of a row have a place of their own, read back by the lane that copied them, so
     // that a wait for its own copies is all the ordering there is
     uint8_t *ring = smem + ((threadIdx.x >> 5) * kPrepStages * kPrepBatch * 32 + lane) * (8 * sizeof(IO));
     constexpr int kRowBytes = 32 * 8 * sizeof(IO);
-    const int64_t D = p.D;
-    // rows [from, from + kPrepBatch) into a stage
+    // the run's rows [from, from + kPrepBatch) into a stage
     auto fetch = [&](int from, int stage) {
         uint8_t *d = ring + stage * (kPrepBatch * kRowBytes);
         const IO *src = x + from * D;
 #pragma unroll
         for (int i = 0; i < kPrepBatch; ++i)
-            if (i < end - from) {
+            if (from + i < r.count) {
                 copy16_async(d + i * kRowBytes, src + i * D);
                 if constexpr (sizeof(IO) == 4) copy16_async(d + i * kRowBytes + 16, src + i * D + 4);
             }
         copy_commit();
     };
 #pragma unroll
-    for (int s = 0; s < kPrepStages - 1; ++s) fetch(t + s * kPrepBatch, s);
+    for (int s = 0; s < kPrepStages - 1; ++s) fetch(s * kPrepBatch, s);
 
     float2 w[4][4], bias[4];
     load_weights<IO>(p, chc, w, bias);
     const HeadOut<IO> out = head_out<IO, DH>(p, chc);
 
     // The three inputs before the current token: before a batch's token i the oldest is win[i % 3],
-    // which takes the token's own input in its place.
-    float2 win[3][4];
-    // The sequence of token tt, the batch's token i, begins (or the run does): the inputs before it,
-    // and, with the first token, the state that the sequence leaves.
-    auto enter = [&](int tt, int i) {
-        if (!ok) b = tt + 1;  // this token alone is passed over
-        int slot = -1;
-        if (ok) slot = slot_of(p.slots, n, p.num_slots, p.status, ok);
-        const int pos = tt - a;
-        IO *state = static_cast<IO *>(p.conv_state) + (int64_t)slot * keep * p.D + chc;
+    // which takes the token's own input in its place.  Before the sequence's first token they are the
+    // state's rows; a run of three tokens or more has no other that reaches into the state.
+    float2 win[3][4] = {};
+    if (r.t0 > r.a) {
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-            const int back = 3 - j;  // the input `back` tokens before this one
-            float2(&before)[4] = win[(i + j) % 3];
+        for (int j = 0; j < 3; ++j)
+            if (3 - j <= keep) widen8(raw8(x - (3 - j) * D), win[j]);
+    } else if (r.slot >= 0) {
+        IO *state = static_cast<IO *>(p.conv_state) + (int64_t)r.slot * keep * D + chc;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) before[e] = make_float2(0.f, 0.f);
-            if (ok && back <= keep) {
-                if (pos >= back) widen8(raw8(x + (tt - back) * D), before);
-                else if (slot >= 0) widen8(raw8(state + (keep + pos - back) * D), before);
+        for (int j = 0; j < 3; ++j)
+            if (3 - j <= keep) widen8(raw8(state + (keep - 3 + j) * D), win[j]);
+        if (live) {
+            // The state that the sequence leaves: the last `keep` of the old state and its inputs, oldest
+            // first, so that an old row is read before it is overwritten.
+            const int len = r.b - r.a;
+            for (int i = 0; i < keep; ++i) {
+                const int from = len + i;
+                store_raw8(state + i * D, from < keep ? raw8(state + from * D) : raw8(x + (from - keep) * D));
             }
         }
-        if (ok && pos == 0 && slot >= 0 && live) {
-            // the last `keep` of the old state and the sequence's inputs, oldest first, so that an old
-            // row is read before it is overwritten
-            const int len = b - a;
-            for (int r = 0; r < keep; ++r) {
-                const int from = len + r;
-                const Raw8<IO> row = from < keep ? raw8(state + from * D) : raw8(x + (a + from - keep) * D);
-                float f[8];
-                widen8(row, f);
-                store8(state + r * D, f);
-            }
-        }
-    };
-    const uint8_t *rows = ring;  // of the batch in use
-    // The convolution at the batch's token i, its input from the ring.
-    auto convolve = [&](int i, float2(&y)[4]) {
-        float2 cur[4];
-        widen8(raw8(reinterpret_cast<const IO *>(rows + i * kRowBytes)), cur);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float2 acc = fma2(win[i % 3][e], w[0][e], bias[e]);
-            acc = fma2(win[(i + 1) % 3][e], w[1][e], acc);
-            acc = fma2(win[(i + 2) % 3][e], w[2][e], acc);
-            y[e] = fma2(cur[e], w[3][e], acc);
-            win[i % 3][e] = cur[e];
-        }
-    };
-    if (t == b) ok = seq_of_token(p, t, n, a, b);
-    enter(t, 0);
+    }
     int stage = 0;
-    IO *o = out.dst + t * out.stride;
-    for (; t < end; t += kPrepBatch) {
+    IO *o = out.dst + r.t0 * out.stride;
+    for (int t = 0; t < r.count; t += kPrepBatch) {
         fetch(t + (kPrepStages - 1) * kPrepBatch, stage == 0 ? kPrepStages - 1 : stage - 1);
         copy_wait<kPrepStages - 1>();
-        rows = ring + stage * (kPrepBatch * kRowBytes);
-        if (t + kPrepBatch <= (b < end ? b : end)) {
-            // the batch lies in one sequence: its tokens side by side, without checks between them
-            float2 y[kPrepBatch][4];
+        const uint8_t *rows = ring + stage * (kPrepBatch * kRowBytes);
+        // a batch's tokens side by side; what the last one computes past the run's end is not stored
+        float2 y[kPrepBatch][4];
 #pragma unroll
-            for (int i = 0; i < kPrepBatch; ++i) convolve(i, y[i]);
-            finish<IO, DH>(p, out, y, o, live && ok);
-        } else {
+        for (int i = 0; i < kPrepBatch; ++i) {
+            float2 cur[4];
+            widen8(raw8(reinterpret_cast<const IO *>(rows + i * kRowBytes)), cur);
 #pragma unroll
-            for (int i = 0; i < kPrepBatch; ++i) {
-                if (t + i >= end) break;
-                if (t + i >= b) {
-                    ok = seq_of_token(p, t + i, n, a, b);
-                    enter(t + i, i);
-                }
-                float2 y[1][4];
-                convolve(i, y[0]);
-                finish<IO, DH>(p, out, y, o + i * out.stride, live && ok);
+            for (int e = 0; e < 4; ++e) {
+                float2 acc = fma2(win[i % 3][e], w[0][e], bias[e]);
+                acc = fma2(win[(i + 1) % 3][e], w[1][e], acc);
+                acc = fma2(win[(i + 2) % 3][e], w[2][e], acc);
+                y[i][e] = fma2(cur[e], w[3][e], acc);
+                win[i % 3][e] = cur[e];
             }
         }
+        finish<IO, DH>(p, out, y, o, live ? r.count - t : 0);
         o += kPrepBatch * out.stride;
         stage = stage + 1 < kPrepStages ? stage + 1 : 0;
     }
@@ -375,7 +334,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32) gdn_prep_step_kernel(const Pr
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[0][e] = fma2(cur[e], w[3][e], y[0][e]);
     const HeadOut<IO> out = head_out<IO, DH>(p, chc);
-    finish<IO, DH>(p, out, y, out.dst + n * out.stride, live && ok);
+    finish<IO, DH>(p, out, y, out.dst + n * out.stride, live && ok ? 1 : 0);
 }
 
 template <typename IO, int DH>
@@ -399,9 +358,13 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
                          : launch_serialised(gdn_prep_step_kernel<IO, 64>, grid, kPrepWarps * 32, 0, st, p);
     }
     const int64_t want = (int64_t)sm_count_cached() * 16;
+    auto ids = [&] {
+        return p.cu ? p.ntok / p.run + p.N : (int64_t)p.N * (((int64_t)p.T + p.run - 1) / p.run);
+    };
     p.run = 48;
-    while (p.run > 1 && (p.ntok + p.run - 1) / p.run * (p.slabs + 1) < want) p.run = p.run > 3 ? p.run / 2 : 1;
-    const dim3 grid((unsigned)((p.ntok + p.run - 1) / p.run), blocks);
+    while (p.run > 3 && ids() * (p.slabs + 1) < want) p.run /= 2;
+    if (ids() > 0x7fffffffLL) return KKT_ERR_ARG;
+    const dim3 grid((unsigned)ids(), blocks);
     return dh == 128 ? launch<IO, 128>(p, grid, st) : launch<IO, 64>(p, grid, st);
 }
 
