@@ -8,8 +8,8 @@
 // head's sum of squares is a shuffle over its 8 or 16 lanes.  The two gates are one more slab.
 //
 // What bounds it: by bytes HBM (the 27.9k packed tokens of 6144 channels of the bf16 prefill case
-// move 686 MB, 103 us at the copy rate; it takes 128 us, 80%), but 25 output heads' worth of SiLU and
-// norms a token keep the issue slots half busy, so the kernel is written against latency:
+// move 686 MB, 103 us at the copy rate; it takes 128 us, 80%), but the arithmetic keeps the issue slots
+// more than half busy, so the kernel is written against latency and instructions:
 //   - the inputs go through a ring of rows in shared memory by asynchronous copies, nine rows ahead,
 //     each lane reading back what it copied itself (no barrier), so that no registers wait on memory;
 //   - three tokens, the window's turn, are computed side by side, and pairs of channels share one
@@ -288,9 +288,11 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
 }
 
 // A decode step, one token for every sequence: a warp has one sequence's token, with nothing to slide
-// over.  The state's rows wait for the slot alone; everything else is loaded beside it.
+// over.  The state's rows wait for the slot alone; everything else is loaded beside it.  Bound by that
+// chain of two loads and, with many sequences, by HBM: of 8192 channels in bf16, 64 sequences 3.2 us
+// (their bytes take 1.3), 256 8.7 us (5.1), 2048 52 us (40).
 template <typename IO, int DH>
-__global__ void __launch_bounds__(kPrepWarps * 32) gdn_prep_step_kernel(const PrepParams p) {
+__global__ void __launch_bounds__(kPrepWarps * 32, sizeof(IO) == 2 ? 14 : 10) gdn_prep_step_kernel(const PrepParams p) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
