@@ -1,7 +1,7 @@
 // binding.cpp -- the Python binding of the serving operators (include/gdn_layer.h): argument checks,
 // output allocation, and the calls into libkkt.so on torch's current stream.  A decode step makes
 // these calls for every layer and token with kernels of a few microseconds, so the marshalling is
-// native: through ctypes a call took 16 to 45 us of the host's time, see layer.py.
+// native: a call takes 3.5 to 8 us of the host's time, and took 16 to 68 through ctypes.
 //
 // A function returns its outputs, or as an int the kkt_status of a refused call, or, negated, what a
 // checked call found in the device's status word; what the arguments themselves show to be wrong raises
