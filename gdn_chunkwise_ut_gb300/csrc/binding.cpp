@@ -124,6 +124,9 @@ PyObject *guarded(F f) {
     HANDLE_TH_ERRORS
     try {
         return f();
+    } catch (python_error &e) {  // Python's own error, set where it was met
+        e.persist();
+        throw;
     } catch (const Refusal &r) {
         PyErr_SetString(PyExc_ValueError, r.what.c_str());
         return nullptr;
@@ -141,7 +144,9 @@ PyObject *trouble(int rc, PyObject *check, CUstream_st *stream) {
         const char *env = std::getenv("KKT_CHECK");
         checked = env && std::strcmp(env, "1") == 0;
     } else if (!checked) {
-        checked = PyObject_IsTrue(check) == 1;
+        const int truth = PyObject_IsTrue(check);
+        if (truth < 0) throw python_error();
+        checked = truth != 0;
     }
     if (checked && (rc = kkt_device_status(stream)) != KKT_OK) return PyLong_FromLong(-rc);
     return nullptr;
@@ -216,7 +221,7 @@ PyObject *prep(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int Hk = integer(a[7], "Hk"), Hv = integer(a[8], "Hv"), dk = integer(a[9], "dk"), dv = integer(a[10], "dv");
         const Tensor bias = optional(a[11], "bias"), slots = optional(a[12], "slots"), cu = optional(a[13], "cu_seqlens");
         const int expand = PyObject_IsTrue(a[14]);
-        if (expand < 0) return nullptr;
+        if (expand < 0) throw python_error();
         const double eps = number(a[15], "eps");
         const char *shapes = "x [B,T,D], weight [D,taps], conv_state [P,taps-1,D]";
         need_dim(x, shapes, 3); need_dim(weight, shapes, 2); need_dim(conv, shapes, 3);

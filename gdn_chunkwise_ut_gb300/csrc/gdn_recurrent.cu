@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kRecWarps * 32) gdn_recurrent_kernel(const Rec
     for (int i = 0; i < kShare; ++i) {
         const int e = i * 32 + lane;  // piece e of k, then of q
         src[i] = static_cast<const IO *>(e < KC ? p.k : p.q) + k_at + (e < KC ? e : e - KC) * V;
-        dst[i] = e * V;  // q lies behind k
+        dst[i] = e * V;  // values from the token's place on: q lies behind k
     }
     const IO *vsrc = static_cast<const IO *>(p.v) + s.a * v_step + (int64_t)h * DV + col0 + lane * V;
     const float *gsrc = lane == VC ? p.beta : lane == VC + 1 ? p.g : nullptr;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kRecWarps * 32) gdn_recurrent_kernel(const Rec
             Token<IO, DK> &x = ring[t & (kRecRing - 1)];
 #pragma unroll
             for (int i = 0; i < kShare; ++i) {
-                if (2 * KC >= 32 || lane < 2 * KC) copy16_async(x.k + dst[i], src[i]);
+                if (2 * KC >= 32 || lane < 2 * KC) copy16_async(reinterpret_cast<IO *>(&x) + dst[i], src[i]);
                 src[i] += k_step;
             }
             if (lane < VC) copy16_async(x.v + lane * V, vsrc);
