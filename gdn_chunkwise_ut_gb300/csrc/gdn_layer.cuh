@@ -125,7 +125,8 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
         : "=l"(reinterpret_cast<uint64_t &>(d))
         : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
     return d;
-}__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
     float2 d;
     asm("add.rn.f32x2 %0, %1, %2;"
         : "=l"(reinterpret_cast<uint64_t &>(d))
@@ -209,8 +210,8 @@ struct Span {
 };
 __device__ __forceinline__ Span seq_span(const int32_t *cu, int n, int N, int T, int64_t ntok, int *status) {
     Span s;
-    s.a = seq_start(cu, n, T);
-    s.b = seq_start(cu, n + 1, T);
+    s.a = cu ? (int64_t)cu[n] : (int64_t)n * T;
+    s.b = cu ? (int64_t)cu[n + 1] : (int64_t)(n + 1) * T;
     s.ok = s.a >= 0 && s.b >= s.a && s.b <= ntok && (n > 0 || s.a == 0) && (n < N - 1 || s.b == ntok);
     if (!s.ok) record_error(status, KKT_ERR_SEQLENS);
     return s;
@@ -218,7 +219,7 @@ __device__ __forceinline__ Span seq_span(const int32_t *cu, int n, int N, int T,
 
 // The slot of sequence n: negative: none; ok is false (and the error recorded) past the pool's end.
 __device__ __forceinline__ int slot_of(const int32_t *slots, int n, int num_slots, int *status, bool &ok) {
-    const int s = slots ? __ldg(slots + n) : n;
+    const int s = slots ? slots[n] : n;
     if (s >= num_slots) {
         record_error(status, KKT_ERR_INDEX);
         ok = false;
@@ -240,7 +241,9 @@ inline int sm_count_cached() {
 }
 
 // Launch whose blocks may be scheduled while the previous kernel on the stream finishes; the kernel
-// waits (griddep_wait) before it touches global memory.
+// waits (griddep_wait) before it touches global memory.  What it reads may be written while it is
+// already resident, so nothing is read through the read-only path (ld.global.nc), which the compiler
+// may move ahead of that wait.
 template <typename... Params, typename... Args>
 inline int launch_serialised(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                              Args... args) {

@@ -64,7 +64,7 @@ __device__ __forceinline__ bool run_of(const PrepParams &p, int id, Run &r) {
         int lo = 0, hi = p.N - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)(__ldg(p.cu + mid) / p.run) + mid <= id) lo = mid; else hi = mid - 1;
+            if ((int64_t)(p.cu[mid] / p.run) + mid <= id) lo = mid; else hi = mid - 1;
         }
         const Span s = seq_span(p.cu, lo, p.N, p.T, p.ntok, p.status);
         if (!s.ok) return false;
@@ -87,10 +87,10 @@ __device__ __forceinline__ void gates(const PrepParams &p, int64_t first, int64_
     for (int64_t i = first + lane; i < first + count; i += 32) {
         const int h = (int)(i % p.Hv);
         const float bb = to_f32(static_cast<const IO *>(p.b)[i]);
-        const float u = to_f32(static_cast<const IO *>(p.a)[i]) + __ldg(p.dt_bias + h);
+        const float u = to_f32(static_cast<const IO *>(p.a)[i]) + p.dt_bias[h];
         p.beta[i] = 1.f / (1.f + expf(-bb));
         // softplus(u) = max(u, 0) + log(1 + e^-|u|); a NaN stays one
-        p.g[i] = -expf(__ldg(p.A_log + h)) * ((u > 0.f ? u : u < 0.f ? 0.f : u) + log1pf(expf(-fabsf(u))));
+        p.g[i] = -expf(p.A_log[h]) * ((u > 0.f ? u : u < 0.f ? 0.f : u) + log1pf(expf(-fabsf(u))));
     }
 }
 
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
     const int slab = blockIdx.y * kPrepWarps + (threadIdx.x >> 5);
     if (slab > p.slabs) return;
     if (slab == p.slabs && blockIdx.x == 0 && p.cu)
-        for (int n = lane; n < p.N; n += 32) check_sequence(p.cu, n, p.N, p.ntok, p.status);
+        for (int n = lane; n < p.N; n += 32) seq_span(p.cu, n, p.N, p.T, p.ntok, p.status);  // records what is malformed
     Run r;
     if (!run_of(p, blockIdx.x, r)) return;
     if (slab == p.slabs) {

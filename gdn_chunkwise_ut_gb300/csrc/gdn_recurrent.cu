@@ -110,12 +110,15 @@ __global__ void __launch_bounds__(kRecWarps * 32, sizeof(ST) == 4 ? 4 : 3) gdn_r
     using Row = std::conditional_t<sizeof(ST) == 4, float4, uint4>;
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t warp = (int64_t)blockIdx.x * kRecWarps + (threadIdx.x >> 5);
-    const int64_t pair = warp / kParts;
-    if (pair >= (int64_t)p.N * p.Hv) return;
-    const int n = (int)(pair / p.Hv), h = (int)(pair % p.Hv);
+    // a block has a part of one (sequence, head), or several of them whole
+    constexpr int kBlocks = kParts > kRecWarps ? kParts / kRecWarps : 1, kPairs = kParts < kRecWarps ? kRecWarps / kParts : 1;
+    const int warp = threadIdx.x >> 5;
+    const int pair = (int)(blockIdx.x / kBlocks) * kPairs + warp / kParts;
+    const int part = (blockIdx.x % kBlocks) * kRecWarps + warp % kParts;
+    if (pair >= p.N * p.Hv) return;
+    const int n = pair / p.Hv, h = pair % p.Hv;
     const int lane = threadIdx.x & 31, r = lane >> 2, row0 = r * R;
-    const int col = (int)(warp % kParts) * 4 * C + (lane & 3) * C;  // the lane's first column
+    const int col = part * 4 * C + (lane & 3) * C;  // the lane's first column
     const int own = col + (r & 3) * E;                             // the first whose sum it ends up with
     bool ok = true;
     const int in = slot_of(p.slots, n, p.num_slots, p.status, ok);
@@ -129,9 +132,9 @@ __global__ void __launch_bounds__(kRecWarps * 32, sizeof(ST) == 4 ? 4 : 3) gdn_r
     }
     float v[E];
 #pragma unroll
-    for (int c = 0; c < E; ++c) v[c] = to_f32(static_cast<const IO *>(p.v)[pair * DV + own + c]);
-    const float beta = __ldg(p.beta + pair);
-    const float a = p.g ? expf(__ldg(p.g + pair)) : 1.f;
+    for (int c = 0; c < E; ++c) v[c] = to_f32(static_cast<const IO *>(p.v)[(int64_t)pair * DV + own + c]);
+    const float beta = p.beta[pair];
+    const float a = p.g ? expf(p.g[pair]) : 1.f;
     if (!ok) return;
     const int64_t off = ((int64_t)h * DK + row0) * DV + col, slot_size = (int64_t)p.Hv * DK * DV;
     Row S[R] = {};
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kRecWarps * 32, sizeof(ST) == 4 ? 4 : 3) gdn_r
     token_update<C>(zs, ys, kq.x + kq.y, v, beta, a, p.scale, lane, d, o);
     if (r & 4) {
 #pragma unroll
-        for (int c = 0; c < E; ++c) static_cast<IO *>(p.o)[pair * DV + own + c] = from_f32<IO>(o[c]);
+        for (int c = 0; c < E; ++c) static_cast<IO *>(p.o)[(int64_t)pair * DV + own + c] = from_f32<IO>(o[c]);
     }
     if (out < 0) return;
 #pragma unroll
@@ -349,7 +352,7 @@ extern "C" int gdn_recurrent_fwd(const void *q, const void *k, const void *v, co
         return KKT_ERR_ARG;
     if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return KKT_ERR_UNSUPPORTED;
     const int64_t ntok = cu_seqlens ? (int64_t)T : (int64_t)N * T;
-    if (ntok > 0x7fffffffLL || (int64_t)N * Hv * (dv / 16 / kRecWarps) > 0x7fffffffLL) return KKT_ERR_ARG;
+    if (ntok > 0x7fffffffLL || (int64_t)N * Hv * (dv / 16 / kRecWarps) > 0x7ffffff0LL) return KKT_ERR_ARG;
     if (ntok > 0 && (!q || !k || !v || !beta || !o)) return KKT_ERR_ARG;
     if (num_slots > 0 && !state) return KKT_ERR_ARG;
     if (!slots && N > num_slots) return KKT_ERR_ARG;

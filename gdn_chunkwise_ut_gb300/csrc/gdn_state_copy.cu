@@ -32,8 +32,8 @@ __global__ void __launch_bounds__(kCopyThreads) state_copy_kernel(const __grid_c
     const CopyTensor &t = p.t[i];
     const size_t first = (size_t)(blockIdx.x - (i ? p.end[i - 1] : 0u)) * kCopyPiece;
     const int m = blockIdx.y;
-    const int d = __ldg(p.dst_slots + m);
-    const int s = p.src_slots && t.src ? __ldg(p.src_slots + m) : -1;
+    const int d = p.dst_slots[m];
+    const int s = p.src_slots && t.src ? p.src_slots[m] : -1;
     if (d >= p.dst_num || s >= p.src_num) {
         record_error(p.status, KKT_ERR_INDEX);
         return;
