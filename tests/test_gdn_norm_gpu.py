@@ -161,3 +161,25 @@ def test_refusals():
         gated_rms_norm_fwd(randn(2, 96), randn(2, 96), randn(96))
     with pytest.raises(ValueError):
         gated_rms_norm_fwd(randn(2, 128), randn(2, 64), randn(128))
+
+
+@pytest.mark.parametrize("rows,dim", [(2450, 128), (2451, 200), (2449, 513), (2450, 1000), (2447, 1501), (2450, 2048),
+                                      (1300, 2816), (700, 4096), (211, 5697), (310, 8192), (160, 16384), (170, 16383)])
+def test_add_rms_norm_many_rows_of_every_width(rows, dim):
+    """Rows enough that a warp holds four units of one and a block several rows, the last block not full."""
+    for io, out, group in ((torch.bfloat16, torch.bfloat16, 128), (torch.bfloat16, FP8, 128), (torch.float32, FP8, None)):
+        x, r = randn(rows, dim, seed=dim, io=io), randn(rows, dim, seed=2, scale=3.0, io=io)
+        w = (1 + randn(dim, seed=1, scale=0.2, io=torch.float32)).to(io)
+        y, scales, r_out = add_rms_norm_fwd(x, w, r, out_dtype=out, group=group)
+        torch.cuda.synchronize()
+        h = to64(x) + to64(r)
+        check_out(y, scales, norm_ref(h, to64(w)), group or dim)
+        check_rounded(r_out, h, FP32_VALUE, "residual")
+
+
+def test_misaligned_inputs_are_refused():
+    raw, w = randn(257), randn(128)
+    with pytest.raises(_lib.KktError, match="misaligned"):
+        add_rms_norm_fwd(raw[1:].view(2, 128), w)
+    with pytest.raises(_lib.KktError, match="misaligned"):
+        gated_rms_norm_fwd(raw[1:].view(2, 128), randn(2, 128), w)

@@ -200,3 +200,19 @@ def test_refusals():
         gdn_prep_fwd(**make((2, 3), 2, 4, 64, 2, taps=5))
     with pytest.raises(_lib.KktError):
         gdn_prep_fwd(**make((3, 3), 2, 4, 64, 2))        # three sequences, two slots, none named
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+def test_long_prompts(io):
+    """Enough tokens that a warp has a run of 48, of sequences many runs long, beside ones of a few tokens."""
+    lengths = [4000, 1, 700, 95, 48, 3, 0, 49]
+    cu = [int(x) for x in np.concatenate([[0], np.cumsum(lengths)])]
+    run_and_check(make((1, cu[-1]), 16, 16, 128, 9, io=io, seed=41), slots=[8, 3, 5, 7, 1, 0, 2, 6], cu=cu)
+    run_and_check(make((2, 2500), 16, 16, 128, 2, io=io, bias=False, seed=42))
+
+
+def test_misaligned_inputs_are_refused():
+    t = make((1, 3), 1, 1, 64, 1)
+    raw = torch.zeros(t["x"].numel() + 1, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(_lib.KktError, match="misaligned"):
+        gdn_prep_fwd(**dict(t, x=raw[1:].view(t["x"].shape)))

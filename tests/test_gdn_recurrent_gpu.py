@@ -224,3 +224,23 @@ def test_refusals():
         gdn_recurrent_fwd(*make((2, 1), 3, 4, 128, 128, P=2)[:4], state)
     with pytest.raises(_lib.KktError):
         gdn_recurrent_fwd(*make((2, 1), 2, 4, 32, 32, P=2)[:4], make_state(2, 4, 32, 32, device=DEV))
+
+
+@pytest.mark.parametrize("N,Hk,Hv", [(1, 1, 1), (3, 1, 3), (5, 5, 5), (7, 1, 1)])
+def test_one_token_of_an_odd_number_of_heads(N, Hk, Hv):
+    """Blocks of the one-token kernel that hold several (sequence, head) pairs, the last one not full."""
+    for dk, dv in ((128, 64), (64, 64), (64, 128)):
+        for state in (torch.bfloat16, torch.float32):
+            run_and_check(*make((N, 1), Hk, Hv, dk, dv, state=state, P=N + 1, seed=N), slots=list(range(N, 0, -1)))
+
+
+def test_one_token_slots_in_and_out():
+    args = make((4, 1), 2, 4, 128, 128, state=torch.bfloat16, P=9, seed=16)
+    run_and_check(*args, slots=[2, 2, -1, 3], slots_out=[4, 5, 6, -1])
+
+
+def test_misaligned_inputs_are_refused():
+    q, k, v, beta, g, state = make((1, 1), 1, 1, 128, 128, P=1)
+    raw = torch.zeros(129, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(_lib.KktError, match="misaligned"):
+        gdn_recurrent_fwd(raw[1:].view(q.shape), k, v, beta, state, g=g)

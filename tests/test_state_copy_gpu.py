@@ -161,3 +161,18 @@ def test_sources_without_slots_are_out_of_range():
     gdn_state_copy(t, i32([1]), empty, i32([0]))
     torch.cuda.synchronize()
     assert device_status() == _lib.KKT_ERR_INDEX and torch.equal(t, before)
+
+
+def test_pool_on_another_stream():
+    """Every pool call on a stream of the caller's; its index tensors belong to that stream."""
+    pool = StatePool(8, 1, 1, 1, 64, 64)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    a, b = pool.alloc(2, stream=stream)
+    with torch.cuda.stream(stream):
+        pool.states[0][a], pool.states[0][b] = 3.0, 4.0
+    f = pool.fork(b, 3, stream=stream)
+    pool.free([a])
+    moves = pool.compact(stream=stream)
+    stream.synchronize()
+    assert moves == {f[-1]: a} and torch.all(pool.states[0][a] == 4.0) and torch.all(pool.states[0][f[0]] == 4.0)
