@@ -354,6 +354,8 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
     // less often, a shorter one gives more warps: the longest that still fills the SMs (16 warps each).
     // In the prefill case (see the top) runs of 36 tokens take 130 us, 48 128, 96 134.
     const unsigned blocks = (unsigned)((p.slabs + 1 + kPrepWarps - 1) / kPrepWarps);
+    // One token a sequence: the kernel for it against the general one: 64 sequences of 8192 channels 3.2
+    // against 4.7 us, 256 8.7 against 20.8, 2048 52 against 136.
     if (!p.cu && p.T == 1) {
         const dim3 grid((unsigned)p.N, blocks);
         return dh == 128 ? launch_serialised(gdn_prep_step_kernel<IO, 128>, grid, kPrepWarps * 32, 0, st, p)

@@ -324,6 +324,9 @@ __global__ void __launch_bounds__(kRecWarps * 32) gdn_recurrent_kernel(const Rec
 template <typename IO, typename ST, int DK, int DV>
 int launch(const RecParams &p, cudaStream_t st) {
     const int64_t pairs = (int64_t)p.N * p.Hv;
+    // One token a sequence: the kernel for it against the general one: 64 x 32 heads in bf16 states 26.8
+    // against 29.9 us, 256 x 64 184 against 202, fp32 states 43.3 and 309 in either, one sequence of 16
+    // heads 2.8 against 3.1.
     if (!p.cu && p.T == 1) {
         constexpr int kParts = DV * (int)sizeof(ST) / 64;
         const dim3 grid((unsigned)((pairs * kParts + kRecWarps - 1) / kRecWarps));
