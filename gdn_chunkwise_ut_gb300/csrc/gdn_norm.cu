@@ -7,8 +7,9 @@
 // the sum of squares and its use, and are bound by HBM: with the residual, 32768 rows of 4096 take
 // 154.6 us (104% of the copy rate), of 2048 80.0 us (100%), 8 bits out 145 us (97%); the gated one over
 // 32768 x 16 heads 60 us in bf16 (100%) and 55.4 us in 8 bits (91%), where instructions begin to count:
-// pairs of values share them (without, 71.5 us).  Rows whose width is no multiple of 8 are loaded value
-// by value and run at half that rate (8467 rows of 7353, 8 bits out: 123 us for 65 us' bytes).
+// pairs of values share them (without, 71.5 us); the same holds without the residual in 8 bits (32768 x
+// 4096: 91 us where the bytes take 61).  Rows whose width is no multiple of 8 are loaded value
+// by value and run at half that rate (8467 rows of 7353, 8 bits out: 117 us for 65 us' bytes).
 #include "gdn_layer.cuh"
 
 namespace kkt {
@@ -23,8 +24,8 @@ struct NormParams {
     void *y, *r_out;
     float *scales;
     int64_t rows;
-    int dim, group, row_warps;
-    float eps;
+    int dim, group, groups, row_warps;
+    float inv_dim, eps;
 };
 
 // A row is cut into units, each held by one warp.  Where the row's length is a multiple of 8 every row
@@ -116,8 +117,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, NV * Unit<VEC>::P > 32 ? 1 : 
         for (int i = 0; i < U::P; ++i) ss = fma2(h[j][i], h[j][i], ss);
         if (p.r_out) store_unit<VEC>(static_cast<IO *>(p.r_out) + at, e0 + j * step, dim, h[j]);
     }
-    const float r = rsqrtf(row_reduce<false>(ss.x + ss.y, part[0], row_warps) / (float)p.dim + p.eps);
-    const float2 r2 = make_float2(r, r);
+    const float r = rsqrtf(fmaf(row_reduce<false>(ss.x + ss.y, part[0], row_warps), p.inv_dim, p.eps));
     OUT *y = static_cast<OUT *>(p.y) + at;
     float top = 0.f;
 #pragma unroll
@@ -126,35 +126,36 @@ __global__ void __launch_bounds__(kNormWarps * 32, NV * Unit<VEC>::P > 32 ? 1 : 
         float2 w[U::P];
         load_unit<VEC>(static_cast<const IO *>(p.w), e, dim, w);
 #pragma unroll
-        for (int i = 0; i < U::P; ++i) h[j][i] = mul2(mul2(h[j][i], r2), w[i]);
+        for (int i = 0; i < U::P; ++i) h[j][i] = mul2(h[j][i], w[i]);
+        float f = r;  // to the output: r, over the scale in 8 bits
         if constexpr (sizeof(OUT) == 1) {
             float m = 0.f;
 #pragma unroll
             for (int i = 0; i < U::P; ++i) m = fmaxf(m, fmaxf(fabsf(h[j][i].x), fabsf(h[j][i].y)));
-            if (p.group) {
-                float inv;
-                const float s = e4m3_scale(lanes_max<U::group_lanes>(m), inv);
-                if (e % 128 == 0 && e < dim) p.scales[row * ((p.dim + 127) / 128) + e / 128] = s;
-                const float2 inv2 = make_float2(inv, inv);
-#pragma unroll
-                for (int i = 0; i < U::P; ++i) h[j][i] = mul2(h[j][i], inv2);
-            } else {
+            if (!p.group) {
                 top = fmaxf(top, m);
                 continue;  // stored once the row's scale is known
             }
+            float inv;
+            const float s = e4m3_scale(r * lanes_max<U::group_lanes>(m), inv);
+            if (e % 128 == 0 && e < dim) p.scales[row * p.groups + e / 128] = s;
+            f = r * inv;
         }
+        const float2 f2 = make_float2(f, f);
+#pragma unroll
+        for (int i = 0; i < U::P; ++i) h[j][i] = mul2(h[j][i], f2);
         store_unit<VEC>(y, e, dim, h[j]);
     }
     if constexpr (sizeof(OUT) == 1) {
         if (p.group) return;
         float inv;
-        const float s = e4m3_scale(row_reduce<true>(top, part[1], row_warps), inv);
+        const float s = e4m3_scale(r * row_reduce<true>(top, part[1], row_warps), inv);
         if (unit0 == 0 && lane == 0 && dim > 0) p.scales[row] = s;
-        const float2 inv2 = make_float2(inv, inv);
+        const float2 f2 = make_float2(r * inv, r * inv);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
-            for (int i = 0; i < U::P; ++i) h[j][i] = mul2(h[j][i], inv2);
+            for (int i = 0; i < U::P; ++i) h[j][i] = mul2(h[j][i], f2);
             store_unit<VEC>(y, e0 + j * step, dim, h[j]);
         }
     }
@@ -228,6 +229,7 @@ int launch_add(NormParams &p, bool vec, cudaStream_t st) {
     if (vec) {
         if (nv <= 1) return launch_add<IO, OUT, 1, true>(p, st);
         if (nv <= 2) return launch_add<IO, OUT, 2, true>(p, st);
+        if (nv <= 3) return launch_add<IO, OUT, 3, true>(p, st);
         if (nv <= 4) return launch_add<IO, OUT, 4, true>(p, st);
         return launch_add<IO, OUT, 8, true>(p, st);
     }
@@ -285,7 +287,7 @@ extern "C" int add_rms_norm_fwd(const void *x, const void *residual, const void 
     if (rows == 0) return KKT_OK;
     NormParams p;
     p.x = x; p.r = residual; p.z = nullptr; p.w = weight; p.y = y; p.r_out = residual_out; p.scales = scales;
-    p.rows = rows; p.dim = dim; p.group = group; p.row_warps = 1; p.eps = eps;
+    p.rows = rows; p.dim = dim; p.group = group; p.groups = (dim + 127) / 128; p.inv_dim = 1.f / (float)dim; p.row_warps = 1; p.eps = eps;
     const bool vec = dim % 8 == 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return io_dtype == KKT_IO_BF16 ? launch_add<__nv_bfloat16>(p, out_dtype, vec, st)
@@ -305,7 +307,7 @@ extern "C" int gated_rms_norm_fwd(const void *x, const void *z, const void *weig
     if (rows == 0) return KKT_OK;
     NormParams p;
     p.x = x; p.r = nullptr; p.z = z; p.w = weight; p.y = y; p.r_out = nullptr; p.scales = scales;
-    p.rows = rows; p.dim = dim; p.group = 0; p.row_warps = 1; p.eps = eps;
+    p.rows = rows; p.dim = dim; p.group = 0; p.groups = 1; p.inv_dim = 1.f / (float)dim; p.row_warps = 1; p.eps = eps;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return io_dtype == KKT_IO_BF16 ? launch_gated<__nv_bfloat16>(p, out_dtype, st)
                                    : launch_gated<float>(p, out_dtype, st);
