@@ -5,7 +5,7 @@
 // A warp owns a slab of 256 consecutive channels (8 to a lane, 16 bytes of bf16: whole heads, since a
 // head is 64 or 128 channels) of a run of consecutive tokens, and keeps the last three inputs of its
 // channels in registers, so a run reads every input once (plus three before its first token).  A
-// head's sum of squares is a shuffle over its 8 or 16 lanes.  The two gates are one more slab.
+// head's sum of squares is a shuffle over its 8 or 16 lanes.  The gates are slabs of their own, 16 heads each.
 //
 // What bounds it: by bytes HBM (the 27.9k packed tokens of 6144 channels of the bf16 prefill case
 // move 686 MB, 103 us at the copy rate; it takes 128 us, 80%), but the arithmetic keeps the issue slots
@@ -20,6 +20,8 @@
 // The convolution's state is read, and its successor written, by the warp that has the sequence's
 // first token, whichever run holds the last one: the same thread reads and writes each element, so
 // updating the pool in place needs no order between warps.
+#include <cmath>
+
 #include "gdn_layer.cuh"
 
 namespace kkt {
@@ -39,7 +41,7 @@ struct PrepParams {
     const int32_t *cu, *slots;
     void *conv_state, *q, *k, *v;
     float *g, *beta;
-    int N, T, Hk, Hv, D, taps, expand, run, num_slots, slabs, wide_weights;
+    int N, T, Hk, Hv, D, taps, expand, run, num_slots, slabs, gate_slabs, wide_weights;
     int64_t ntok;
     float eps;
     int *status;
@@ -81,16 +83,21 @@ __device__ __forceinline__ bool run_of(const PrepParams &p, int id, Run &r) {
     return ok;
 }
 
-// beta = sigmoid(b) and g = -e^{A_log} softplus(a + dt_bias) of `count` consecutive (token, head) pairs.
+// beta = sigmoid(b) and g = -e^{A_log} softplus(a + dt_bias) of `count` (token, head) pairs from token t0
+// on, every p.gate_slabs-th group of 32 of them from `part` on.
 template <typename IO>
-__device__ __forceinline__ void gates(const PrepParams &p, int64_t first, int64_t count, int lane) {
-    for (int64_t i = first + lane; i < first + count; i += 32) {
-        const int h = (int)(i % p.Hv);
-        const float bb = to_f32(static_cast<const IO *>(p.b)[i]);
-        const float u = to_f32(static_cast<const IO *>(p.a)[i]) + p.dt_bias[h];
-        p.beta[i] = 1.f / (1.f + expf(-bb));
+__device__ __forceinline__ void gates(const PrepParams &p, int t0, int count, int part, int lane) {
+    const int64_t first = (int64_t)t0 * p.Hv;
+    const int stride = 32 * p.gate_slabs, turn = stride % p.Hv;
+    int h = (part * 32 + lane) % p.Hv;
+    for (int i = part * 32 + lane; i < count; i += stride) {
+        const float bb = to_f32(static_cast<const IO *>(p.b)[first + i]);
+        const float u = to_f32(static_cast<const IO *>(p.a)[first + i]) + p.dt_bias[h];
+        p.beta[first + i] = 1.f / (1.f + expf(-bb));
         // softplus(u) = max(u, 0) + log(1 + e^-|u|); a NaN stays one
-        p.g[i] = -expf(p.A_log[h]) * ((u > 0.f ? u : u < 0.f ? 0.f : u) + log1pf(expf(-fabsf(u))));
+        p.g[first + i] = -expf(p.A_log[h]) * ((u > 0.f ? u : u < 0.f ? 0.f : u) + log1pf(expf(-fabsf(u))));
+        h += turn;
+        if (h >= p.Hv) h -= p.Hv;
     }
 }
 
@@ -198,13 +205,13 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int slab = blockIdx.y * kPrepWarps + (threadIdx.x >> 5);
-    if (slab > p.slabs) return;
+    if (slab >= p.slabs + p.gate_slabs) return;
     if (slab == p.slabs && blockIdx.x == 0 && p.cu)
         for (int n = lane; n < p.N; n += 32) seq_span(p.cu, n, p.N, p.T, p.ntok, p.status);  // records what is malformed
     Run r;
     if (!run_of(p, blockIdx.x, r)) return;
-    if (slab == p.slabs) {
-        gates<IO>(p, (int64_t)r.t0 * p.Hv, (int64_t)r.count * p.Hv, lane);
+    if (slab >= p.slabs) {
+        gates<IO>(p, r.t0, r.count * p.Hv, slab - p.slabs, lane);
         return;
     }
     const int ch = slab * kSlab + lane * 8;
@@ -298,9 +305,9 @@ __global__ void __launch_bounds__(kPrepWarps * 32, sizeof(IO) == 2 ? 14 : 10) gd
     const int lane = threadIdx.x & 31;
     const int slab = blockIdx.y * kPrepWarps + (threadIdx.x >> 5);
     const int n = blockIdx.x;
-    if (slab > p.slabs) return;
-    if (slab == p.slabs) {
-        gates<IO>(p, (int64_t)n * p.Hv, p.Hv, lane);
+    if (slab >= p.slabs + p.gate_slabs) return;
+    if (slab >= p.slabs) {
+        gates<IO>(p, n, p.Hv, slab - p.slabs, lane);
         return;
     }
     bool ok = true;
@@ -349,11 +356,9 @@ int launch(const PrepParams &p, dim3 grid, cudaStream_t st) {
 template <typename IO>
 int launch(PrepParams &p, int dh, cudaStream_t st) {
     p.slabs = (p.D + kSlab - 1) / kSlab;
+    p.gate_slabs = (p.Hv + 15) / 16;  // a token's 16 gates take about as long as its 256 channels
     p.wide_weights = aligned_ptr(p.weight, 16);
-    // Tokens of a run: a longer run re-reads fewer of the three inputs before it and loads its weights
-    // less often, a shorter one gives more warps: the longest that still fills the SMs (16 warps each).
-    // In the prefill case (see the top) runs of 36 tokens take 130 us, 48 128, 96 134.
-    const unsigned blocks = (unsigned)((p.slabs + 1 + kPrepWarps - 1) / kPrepWarps);
+    const unsigned blocks = (unsigned)((p.slabs + p.gate_slabs + kPrepWarps - 1) / kPrepWarps);
     // One token a sequence: the kernel for it against the general one: 64 sequences of 8192 channels 3.2
     // against 4.7 us, 256 8.7 against 20.8, 2048 52 against 136.
     if (!p.cu && p.T == 1) {
@@ -361,12 +366,28 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
         return dh == 128 ? launch_serialised(gdn_prep_step_kernel<IO, 128>, grid, kPrepWarps * 32, 0, st, p)
                          : launch_serialised(gdn_prep_step_kernel<IO, 64>, grid, kPrepWarps * 32, 0, st, p);
     }
-    const int64_t want = (int64_t)sm_count_cached() * 16;
+    // Tokens of a run.  A longer one reads fewer inputs before its first token and sets up less often; a
+    // shorter one gives more warps.  The time goes as (tokens + 8) x waves of 16 warps an SM, whole ones
+    // while they are few: so the run with the least of that, sequences taken to be of one length.  Runs of 6, 18, 30 and 48 tokens take, in
+    // us: 207, 150, 133, 127 (27.9k tokens of 6144 channels; 48 taken), 64, 49, 45, 46 (8192 of them; 48),
+    // 14.1, 12.1, 14.6, 19.8 (1000 of 8192 channels; 18), 5.7, 8.0, 9.3, 12.3 (1.3k of 2048; 6).
     auto ids = [&] {
         return p.cu ? p.ntok / p.run + p.N : (int64_t)p.N * (((int64_t)p.T + p.run - 1) / p.run);
     };
-    p.run = 48;
-    while (p.run > 3 && ids() * (p.slabs + 1) < want) p.run /= 2;
+    const int runs[] = {48, 42, 36, 30, 24, 18, 12, 9, 6, 3};
+    const double mean = std::ceil((double)p.ntok / p.N);  // of a sequence
+    double least = 0.;
+    int best = 0;
+    for (int run : runs) {
+        p.run = run;
+        const double waves = (double)ids() * (p.slabs + p.gate_slabs) / (sm_count_cached() * 16);
+        const double cost = (waves > 3. ? waves : std::ceil(waves)) * ((run < mean ? run : mean) + 8);
+        if (best == 0 || cost < least) {
+            least = cost;
+            best = run;
+        }
+    }
+    p.run = best;
     if (ids() > 0x7fffffffLL) return KKT_ERR_ARG;
     const dim3 grid((unsigned)ids(), blocks);
     return dh == 128 ? launch<IO, 128>(p, grid, st) : launch<IO, 64>(p, grid, st);
