@@ -33,6 +33,7 @@ constexpr int kPrepWarps = 2;
 constexpr int kPrepBatch = 3;   // tokens whose inputs are copied together: the window's turn
 constexpr int kPrepStages = 4;  // such copies in flight, with the one in use
 static_assert(kPrepBatch == 3, "the window's registers take turns with the tokens of a batch");
+constexpr int kPrepShort = 4;   // tokens of a short run
 constexpr int kSlab = 256;     // channels of a warp
 
 struct PrepParams {
@@ -50,7 +51,8 @@ struct PrepParams {
 // The tokens of a work id: `count` of sequence n from token t0 on, a run that restarts at every sequence.
 // Packed sequences: sequence s owns the ids from floor(start(s) / run) + s on, at least as many as it has
 // runs (as kkt_internal.cuh numbers chunks); the ids left over are idle.  False for those, and, with the
-// error recorded, where cu_seqlens is malformed or the sequence's slot is past the pool's end.
+// error recorded, where cu_seqlens is malformed or the sequence's slot is past the pool's end.  Called by
+// whole warps.
 struct Run {
     int n, a, b, t0, count, slot;
 };
@@ -63,10 +65,16 @@ __device__ __forceinline__ bool run_of(const PrepParams &p, int id, Run &r) {
         r.b = r.a + p.T;
         r.t0 = r.a + (id - r.n * per) * p.run;
     } else {
-        int lo = 0, hi = p.N - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)(p.cu[mid] / p.run) + mid <= id) lo = mid; else hi = mid - 1;
+        // the last sequence whose first id is not past this one, by the warp's 32 lanes at a time: two
+        // loads one behind the other for up to 1024 sequences, where halving takes ten
+        int lo = 0;
+        for (int len = p.N; len > 1;) {
+            const int step = (len + 31) / 32, at = (int)(threadIdx.x & 31) * step;
+            const int s = lo + at;
+            const unsigned not_past = __ballot_sync(0xffffffffu, at < len && (int64_t)(p.cu[at < len ? s : lo] / p.run) + s <= id);
+            const int last = not_past ? 31 - __clz(not_past) : 0;
+            lo += last * step;
+            len = len - last * step < step ? len - last * step : step;
         }
         const Span s = seq_span(p.cu, lo, p.N, p.T, p.ntok, p.status);
         if (!s.ok) return false;
@@ -294,56 +302,94 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
     }
 }
 
-// A decode step, one token for every sequence: a warp has one sequence's token, with nothing to slide
-// over.  The state's rows wait for the slot alone; everything else is loaded beside it.  Bound by that
-// chain of two loads and, with many sequences, by HBM: of 8192 channels in bf16, 64 sequences 3.2 us
-// (their bytes take 1.3), 256 8.7 us (5.1), 2048 52 us (40).
-template <typename IO, int DH>
-__global__ void __launch_bounds__(kPrepWarps * 32, sizeof(IO) == 2 ? 14 : 10) gdn_prep_step_kernel(const PrepParams p) {
+// Runs of a few tokens: R 1 a decode step, one token for every sequence (block x is the sequence), else
+// work ids of up to R tokens.  All of a run's inputs are loaded at once, beside the state's rows, which
+// wait for the slot alone; then a token at a time, in few registers.  Bound by that chain of loads and,
+// with many sequences, by HBM: of 8192 channels in bf16, a token for 64 sequences takes 3.2 us (the bytes
+// 1.3), for 256 8.5 us (5.1), for 2048 51 us (40), four for 256 13.4 us (8.9).
+template <typename IO, int DH, int R>
+__global__ void __launch_bounds__(kPrepWarps * 32, sizeof(IO) == 2 ? (R == 1 ? 14 : 10) : (R == 1 ? 10 : 7))
+    gdn_prep_short_kernel(const PrepParams p) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int slab = blockIdx.y * kPrepWarps + (threadIdx.x >> 5);
-    const int n = blockIdx.x;
     if (slab >= p.slabs + p.gate_slabs) return;
+    Run r;
+    if constexpr (R == 1) {
+        bool ok = true;
+        r.n = r.a = r.t0 = (int)blockIdx.x;
+        r.b = r.a + 1;
+        r.count = 1;
+        r.slot = slot_of(p.slots, r.n, p.num_slots, p.status, ok);
+        if (!ok) return;
+    } else {
+        if (slab == p.slabs && blockIdx.x == 0 && p.cu)
+            for (int n = lane; n < p.N; n += 32) seq_span(p.cu, n, p.N, p.T, p.ntok, p.status);  // records what is malformed
+        if (!run_of(p, blockIdx.x, r)) return;
+    }
     if (slab >= p.slabs) {
-        gates<IO>(p, n, p.Hv, slab - p.slabs, lane);
+        gates<IO>(p, r.t0, r.count * p.Hv, slab - p.slabs, lane);
         return;
     }
-    bool ok = true;
-    const int slot = slot_of(p.slots, n, p.num_slots, p.status, ok);
     const int ch = slab * kSlab + lane * 8;
     const bool live = ch < p.D;
     const int chc = live ? ch : 0;
-    const int64_t D = p.D;
-    const Raw8<IO> in = raw8(static_cast<const IO *>(p.x) + n * D + chc);
-    float2 w[4][4], y[1][4];
-    load_weights<IO>(p, chc, w, y[0]);
     const int keep = p.taps - 1;
-    float2 cur[4];
-    if (ok && slot >= 0) {
-        IO *state = static_cast<IO *>(p.conv_state) + (int64_t)slot * keep * D + chc;
-        Raw8<IO> row[3];
+    const int64_t D = p.D;
+    const IO *x = static_cast<const IO *>(p.x) + r.t0 * D + chc;
+    Raw8<IO> row[3 + R] = {};  // the three inputs before the run, oldest first, and the run's
 #pragma unroll
-        for (int r = 0; r < 3; ++r)
-            if (r < keep) row[r] = raw8(state + r * D);
+    for (int i = 0; i < R; ++i)
+        if (i < r.count) row[3 + i] = raw8(x + i * D);
+    float2 w[4][4], bias[4];
+    load_weights<IO>(p, chc, w, bias);
+    if (r.t0 > r.a) {
 #pragma unroll
-        for (int r = 0; r < 3; ++r)
-            if (r < keep) {
-                widen8(row[r], cur);
-                const int j = r + 4 - p.taps;  // the row's tap
+        for (int j = 0; j < 3; ++j)
+            if (3 - j <= keep) row[j] = raw8(x - (3 - j) * D);
+    } else if (r.slot >= 0) {
+        IO *state = static_cast<IO *>(p.conv_state) + (int64_t)r.slot * keep * D + chc;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[0][e] = fma2(cur[e], j == 0 ? w[0][e] : j == 1 ? w[1][e] : w[2][e], y[0][e]);
-                // the rows move up by one, the token's input behind them
-                if (live) store_raw8(state + r * D, r + 1 < keep ? row[r + 1] : in);
-            }
+        for (int j = 0; j < 3; ++j)
+            if (3 - j <= keep) row[j] = raw8(state + (keep - 3 + j) * D);
+        if (live) {
+            // the state that the sequence leaves: its last inputs, in a short sequence behind the old
+            // state's last rows
+            const int len = r.b - r.a;
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (3 - j <= keep) {
+                    const int from = j + len;  // the row in its place, counted as `row` counts
+                    Raw8<IO> v;
+                    if (len > R) {
+                        v = raw8(x + (from - 3) * D);
+                    } else {
+                        v = row[j + 1];
+#pragma unroll
+                        for (int l = 2; l <= R; ++l)
+                            if (len == l) v = row[j + l];
+                    }
+                    store_raw8(state + (keep - 3 + j) * D, v);
+                }
+        }
     }
-    // the token's own tap last, as in a longer run: a prompt and its decode steps round alike
-    widen8(in, cur);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[0][e] = fma2(cur[e], w[3][e], y[0][e]);
     const HeadOut<IO> out = head_out<IO, DH>(p, chc);
-    finish<IO, DH>(p, out, y, out.dst + n * out.stride, live && ok ? 1 : 0);
+    IO *o = out.dst + r.t0 * out.stride;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (i >= r.count) break;
+        float2 y[1][4], cur[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[0][e] = bias[e];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            widen8(row[i + j], cur);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[0][e] = fma2(cur[e], w[j][e], y[0][e]);
+        }
+        finish<IO, DH>(p, out, y, o + i * out.stride, live ? 1 : 0);
+    }
 }
 
 template <typename IO, int DH>
@@ -353,19 +399,22 @@ int launch(const PrepParams &p, dim3 grid, cudaStream_t st) {
     return launch_serialised(gdn_prep_kernel<IO, DH>, grid, kPrepWarps * 32, smem, st, p);
 }
 
+template <typename IO, int R>
+int launch_short(const PrepParams &p, int dh, dim3 grid, cudaStream_t st) {
+    return dh == 128 ? launch_serialised(gdn_prep_short_kernel<IO, 128, R>, grid, kPrepWarps * 32, 0, st, p)
+                     : launch_serialised(gdn_prep_short_kernel<IO, 64, R>, grid, kPrepWarps * 32, 0, st, p);
+}
+
 template <typename IO>
 int launch(PrepParams &p, int dh, cudaStream_t st) {
     p.slabs = (p.D + kSlab - 1) / kSlab;
     p.gate_slabs = (p.Hv + 15) / 16;  // a token's 16 gates take about as long as its 256 channels
     p.wide_weights = aligned_ptr(p.weight, 16);
     const unsigned blocks = (unsigned)((p.slabs + p.gate_slabs + kPrepWarps - 1) / kPrepWarps);
-    // One token a sequence: the kernel for it against the general one: 64 sequences of 8192 channels 3.2
-    // against 4.7 us, 256 8.7 against 20.8, 2048 52 against 136.
-    if (!p.cu && p.T == 1) {
-        const dim3 grid((unsigned)p.N, blocks);
-        return dh == 128 ? launch_serialised(gdn_prep_step_kernel<IO, 128>, grid, kPrepWarps * 32, 0, st, p)
-                         : launch_serialised(gdn_prep_step_kernel<IO, 64>, grid, kPrepWarps * 32, 0, st, p);
-    }
+    // Short runs against long ones, of 8192 channels: one token for 64 sequences 3.2 against 4.7 us, for 256
+    // 8.5 against 20.8, for 2048 51 against 136; four tokens for 256 13.4 against 18.5, three for 2048 92
+    // against 111; 256 packed sequences of one token 13.8 against 20.7.
+    if (!p.cu && p.T == 1) return launch_short<IO, 1>(p, dh, dim3((unsigned)p.N, blocks), st);
     // Tokens of a run.  A longer one reads fewer inputs before its first token and sets up less often; a
     // shorter one gives more warps.  The time goes as (tokens + 8) x waves of 16 warps an SM, whole ones
     // while they are few: so the run with the least of that, sequences taken to be of one length.  Runs of 6, 18, 30 and 48 tokens take, in
@@ -374,8 +423,13 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
     auto ids = [&] {
         return p.cu ? p.ntok / p.run + p.N : (int64_t)p.N * (((int64_t)p.T + p.run - 1) / p.run);
     };
-    const int runs[] = {48, 42, 36, 30, 24, 18, 12, 9, 6, 3};
     const double mean = std::ceil((double)p.ntok / p.N);  // of a sequence
+    if (mean <= kPrepShort) {
+        p.run = kPrepShort;
+        if (ids() > 0x7fffffffLL) return KKT_ERR_ARG;
+        return launch_short<IO, kPrepShort>(p, dh, dim3((unsigned)ids(), blocks), st);
+    }
+    const int runs[] = {48, 42, 36, 30, 24, 18, 12, 9, 6, 3};
     double least = 0.;
     int best = 0;
     for (int run : runs) {

@@ -52,6 +52,18 @@ def test_packed_sequences_of_every_length(io, taps, d, expand):
     run_and_check(t, slots=[(7 * n + 3) % 20 for n in range(len(lengths))], cu=cu, expand=expand)
 
 
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("taps", [2, 3, 4])
+@pytest.mark.parametrize("d,expand", [(128, True), (64, False)])
+def test_packed_short_sequences(io, taps, d, expand):
+    """Four tokens a sequence on average and less: runs of four, sequences of none to 25 tokens."""
+    lengths = [1] * 12 + [0] * 4 + [2, 3, 4, 5, 6, 7, 4, 3] + [0, 25, 9]
+    cu = [int(x) for x in np.concatenate([[0], np.cumsum(lengths)])]
+    slots = [(5 * n + 2) % 31 if n % 9 else -1 for n in range(len(lengths))]
+    run_and_check(make((1, cu[-1]), 2, 4, d, 31, io=io, taps=taps, bias=taps != 2, seed=60 + taps), slots=slots, cu=cu,
+                  expand=expand)
+
+
 @pytest.mark.parametrize("length", [1, 2, 3, 4, 5, 6, 15, 16, 17, 33])
 def test_many_sequences_of_one_length(length):
     """Enough tokens that a warp has a run of 16: the sequences start at every place of a run, and those
