@@ -8,7 +8,7 @@
 // head's sum of squares is a shuffle over its 8 or 16 lanes.  The gates are slabs of their own, 16 heads each.
 //
 // What bounds it: by bytes HBM (the 27.9k packed tokens of 6144 channels of the bf16 prefill case
-// move 686 MB, 103 us at the copy rate; it takes 128 us, 80%), but the arithmetic keeps the issue slots
+// move 686 MB, 103 us at the copy rate; it takes 126.7 us, 81%), but the arithmetic keeps the issue slots
 // more than half busy, so the kernel is written against latency and instructions:
 //   - the inputs go through a ring of rows in shared memory by asynchronous copies, nine rows ahead,
 //     each lane reading back what it copied itself (no barrier), so that no registers wait on memory;
