@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(kGcThreads, 1)
     griddep_wait();
 
     // this CTA's sequence
-    const int64_t a = p.cu ? (int64_t)__ldg(p.cu + seq) : (int64_t)seq * p.T;
-    const int64_t b = p.cu ? (int64_t)__ldg(p.cu + seq + 1) : (int64_t)(seq + 1) * p.T;
+    const int64_t a = p.cu ? (int64_t)p.cu[seq] : (int64_t)seq * p.T;
+    const int64_t b = p.cu ? (int64_t)p.cu[seq + 1] : (int64_t)(seq + 1) * p.T;
     bool seq_ok = a >= 0 && b >= a && b <= p.ntok;
     if (p.cu && ((seq == 0 && a != 0) || (seq == p.nseq - 1 && b != p.ntok))) seq_ok = false;
     if (!seq_ok && threadIdx.x == 0 && h == 0) record_error(p.status, KKT_ERR_SEQLENS);
@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(kGcThreads, 1)
             constexpr float kLog2e = 1.4426950408889634f;
             float g0 = 0.f, g1 = 0.f;
             if constexpr (GATED) {
-                if (lane < Lc) g0 = kLog2e * __ldg(p.g + (t0 + lane) * p.H + h);
-                if (lane + 32 < Lc) g1 = kLog2e * __ldg(p.g + (t0 + lane + 32) * p.H + h);
+                if (lane < Lc) g0 = kLog2e * p.g[(t0 + lane) * p.H + h];
+                if (lane + 32 < Lc) g1 = kLog2e * p.g[(t0 + lane + 32) * p.H + h];
             }
             if (!gc_wait(&bars->empty[s], (((uint32_t)c >> 1) & 1u) ^ 1u, bars, p.status)) { ok = false; break; }
             if (lane == 0) {
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kGcThreads, 1)
             const int d0 = 64 * hc + 16 * piece;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                v[e] = p.h0 ? __float_as_uint(__ldg(p.h0 + state_base + (int64_t)(d0 + e) * kGcD + row)) : 0u;
+                v[e] = p.h0 ? __float_as_uint(p.h0[state_base + (int64_t)(d0 + e) * kGcD + row]) : 0u;
             tmem_st16(tmem + lane_base + kColS + d0, v);
         }
         tmem_wait_st();

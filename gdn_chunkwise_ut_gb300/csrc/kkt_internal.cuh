@@ -65,7 +65,7 @@ struct Chunk {
 };
 
 __device__ __forceinline__ int64_t seq_start(const int32_t *cu, int s, int T) {
-    return cu ? (int64_t)__ldg(cu + s) : (int64_t)s * T;
+    return cu ? (int64_t)cu[s] : (int64_t)s * T;
 }
 
 __host__ __device__ __forceinline__ int64_t total_work_ids(int64_t ntok, int C, int nseq) {
@@ -105,7 +105,7 @@ __device__ __forceinline__ bool map_chunk(int64_t id, const int32_t *cu, int nse
 // Checks the global shape of cu_seqlens for sequence s (called once per s).
 __device__ __forceinline__ void check_sequence(const int32_t *cu, int s, int nseq, int64_t ntok, int *status) {
     if (!cu) return;
-    const int64_t a = __ldg(cu + s), b = __ldg(cu + s + 1);
+    const int64_t a = cu[s], b = cu[s + 1];
     bool bad = (a < 0) || (b < a) || (b > ntok);
     if (s == 0 && a != 0) bad = true;
     if (s == nseq - 1 && b != ntok) bad = true;

@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) {
                 const int idx = lane + 32 * e;
                 const int g = idx / C, r = idx % C;
-                bv[e] = (r < ch.Lc && h0 + g < p.H) ? __ldg(gmem_chk(p.beta, (ch.t0 + r) * p.H + h0 + g, p.ntok * p.H)) : 0.f;
+                bv[e] = (r < ch.Lc && h0 + g < p.H) ? *gmem_chk(p.beta, (ch.t0 + r) * p.H + h0 + g, p.ntok * p.H) : 0.f;
             }
             // gated: prefix sums G of the log decays over each head's chunk, in log2 units, so that
             // Gamma[i][j] = exp2(G_i - G_j).  For a column j of 32-row block b, with R_b = G at the
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 4; ++e) {
                     const int idx = lane + 32 * e;
                     const int g = idx / C, r = idx % C;
-                    gv[e] = (r < ch.Lc && h0 + g < p.H) ? kLog2e * __ldg(gmem_chk(p.g, (ch.t0 + r) * p.H + h0 + g, p.ntok * p.H)) : 0.f;
+                    gv[e] = (r < ch.Lc && h0 + g < p.H) ? kLog2e * *gmem_chk(p.g, (ch.t0 + r) * p.H + h0 + g, p.ntok * p.H) : 0.f;
                 }
             }
             const int s = i % kNS;
