@@ -60,6 +60,31 @@ void check(const Tensor &t, const char *name, ScalarType dtype, at::IntArrayRef 
     refuse(n + " must be contiguous");
 }
 
+// Checks a tensor that may also be a slice of a larger one: its last dimensions, `packed` values together,
+// lie behind one another, and those before them are one axis of equal steps.  Returns the step.
+int64_t check_sliced(const Tensor &t, const char *name, ScalarType dtype, at::IntArrayRef shape, int64_t packed,
+                     c10::Device dev) {
+    if (t.is_cuda() && t.device() == dev && t.scalar_type() == dtype && t.sizes() == shape && !t.is_contiguous()) {
+        int64_t inner = 1, step = 0, next = 0;  // next: the stride of the outer axis's next dimension
+        bool ok = true;
+        for (int64_t d = t.dim() - 1; d >= 0 && ok; --d) {
+            const int64_t size = t.size(d), stride = t.stride(d);
+            if (inner < packed) {
+                ok = size == 1 || stride == inner;
+                inner *= size;
+            } else if (size > 1) {
+                if (step == 0) step = next = stride;
+                ok = stride == next && step >= packed;
+                next *= size;
+            }
+        }
+        if (ok && inner == packed && step > 0) return step;
+        refuse(std::string(name) + " must be contiguous, or a slice whose tokens are equal steps apart");
+    }
+    check(t, name, dtype, shape, dev);
+    return packed;
+}
+
 int io_type(const Tensor &t, const char *name) {
     if (t.scalar_type() == at::kBFloat16) return KKT_IO_BF16;
     if (t.scalar_type() == at::kFloat) return KKT_IO_F32;
@@ -232,11 +257,11 @@ PyObject *prep(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const c10::Device dev = device_of(x, "x");
         const ScalarType dt = x.scalar_type();
         const int io = io_type(x, "x");
-        check(x, "x", dt, {B, T, D}, dev);
+        const int64_t x_stride = check_sliced(x, "x", dt, {B, T, D}, D, dev);
         check(weight, "weight", dt, {D, taps}, dev);
         if (bias.defined()) check(bias, "bias", dt, {D}, dev);
-        check(ga, "a", dt, {B, T, Hv}, dev);
-        check(gb, "b", dt, {B, T, Hv}, dev);
+        const int64_t a_stride = check_sliced(ga, "a", dt, {B, T, Hv}, Hv, dev),
+                      b_stride = check_sliced(gb, "b", dt, {B, T, Hv}, Hv, dev);
         check(A_log, "A_log", at::kFloat, {Hv}, dev);
         check(dt_bias, "dt_bias", at::kFloat, {Hv}, dev);
         check(conv, "conv_state", dt, {P, taps - 1, D}, dev);
@@ -248,11 +273,11 @@ PyObject *prep(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Tensor q = empty({B, T, Hq, dk}, dt, dev), k = empty({B, T, Hq, dk}, dt, dev),
                      v = empty({B, T, Hv, dv}, dt, dev), g = empty({B, T, Hv}, at::kFloat, dev),
                      beta = empty({B, T, Hv}, at::kFloat, dev);
-        const int rc = gdn_prep_fwd(raw(x), raw(weight), raw(bias), raw(ga), raw(gb), ptr<float>(A_log),
-                                    ptr<float>(dt_bias), ptr<int32_t>(cu), N, small(T, "T"), Hk, Hv, dk, dv,
-                                    small(taps, "taps"), (float)eps, expand, io, raw(conv), small(P, "P"),
-                                    ptr<int32_t>(slots), raw(q), raw(k), raw(v), ptr<float>(g), ptr<float>(beta),
-                                    stream);
+        const int rc = gdn_prep_fwd(raw(x), x_stride, raw(weight), raw(bias), raw(ga), a_stride, raw(gb), b_stride,
+                                    ptr<float>(A_log), ptr<float>(dt_bias), ptr<int32_t>(cu), N, small(T, "T"), Hk,
+                                    Hv, dk, dv, small(taps, "taps"), (float)eps, expand, io, raw(conv),
+                                    small(P, "P"), ptr<int32_t>(slots), raw(q), raw(k), raw(v), ptr<float>(g),
+                                    ptr<float>(beta), stream);
         if (PyObject *said = trouble(rc, a[16], stream)) return said;
         return wrap_all(q, k, v, g, beta);
     });
@@ -328,7 +353,15 @@ PyObject *gated_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int io = io_type(x, "x");
         const int64_t dim = x.size(-1);
         check(x, "x", dt, x.sizes(), dev);
-        check(z, "z", dt, x.sizes(), dev);
+        // z may be a slice: the dimensions before d that lie behind one another are a token's rows
+        int64_t packed = 1;
+        for (int64_t d = z.dim() - 1; d >= 0 && (z.size(d) == 1 || z.stride(d) == packed); --d) packed *= z.size(d);
+        const int64_t z_stride = check_sliced(z, "z", dt, x.sizes(), packed, dev);
+        int64_t z_rows = 0;
+        if (!z.is_contiguous()) {
+            if (packed % dim != 0) refuse("z's rows must be contiguous");
+            z_rows = packed / dim;
+        }
         check(w, "weight", dt, {dim}, dev);
         int code;
         const ScalarType out = out_type(a[4], x, code);
@@ -338,7 +371,7 @@ PyObject *gated_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Tensor y = empty(x.sizes(), out, dev);
         Tensor scales;
         if (code == GDN_OUT_E4M3) scales = empty(x.sizes().slice(0, x.dim() - 1), at::kFloat, dev);
-        const int rc = gated_rms_norm_fwd(raw(x), raw(z), raw(w), dim ? x.numel() / dim : 0, small(dim, "dim"),
+        const int rc = gated_rms_norm_fwd(raw(x), raw(z), small(z_rows, "z's rows"), z_stride, raw(w), dim ? x.numel() / dim : 0, small(dim, "dim"),
                                           (float)eps, io, code, raw(y), ptr<float>(scales), stream);
         if (PyObject *said = trouble(rc, a[5], stream)) return said;
         return wrap_all(y, scales);

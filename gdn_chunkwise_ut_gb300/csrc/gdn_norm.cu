@@ -23,8 +23,8 @@ struct NormParams {
     const void *x, *r, *z, *w;
     void *y, *r_out;
     float *scales;
-    int64_t rows;
-    int dim, group, groups, row_warps;
+    int64_t rows, z_stride, z_step;
+    int z_rows, z_turn, dim, group, groups, row_warps;
     float inv_dim, eps;
 };
 
@@ -174,14 +174,33 @@ __global__ void __launch_bounds__(256) gated_rms_norm_kernel(const NormParams p)
     const int left = (int)(p.rows - row0 < PER * kGatedRows ? p.rows - row0 : PER * kGatedRows);  // may be negative
     float2 w[4];
     widen8(raw8(static_cast<const IO *>(p.w) + e), w);
-    const IO *px = static_cast<const IO *>(p.x) + row0 * DIM + e, *pz = static_cast<const IO *>(p.z) + row0 * DIM + e;
+    const IO *px = static_cast<const IO *>(p.x) + row0 * DIM + e;
     Raw8<IO> xr[kGatedRows] = {}, zr[kGatedRows] = {};
 #pragma unroll
     for (int i = 0; i < kGatedRows; ++i)
-        if (i * PER < left) {
-            xr[i] = raw8(px + i * PER * DIM);
-            zr[i] = raw8(pz + i * PER * DIM);
+        if (i * PER < left) xr[i] = raw8(px + i * PER * DIM);
+    if (p.z_rows == 0) {
+        const IO *pz = static_cast<const IO *>(p.z) + row0 * DIM + e;
+#pragma unroll
+        for (int i = 0; i < kGatedRows; ++i)
+            if (i * PER < left) zr[i] = raw8(pz + i * PER * DIM);
+    } else {
+        // the row is the head `head` of a token; PER rows on are z_step values and z_turn heads, or, past
+        // the token's last head, that many of the next token's
+        int64_t token = row0 / p.z_rows;
+        int head = (int)(row0 - token * p.z_rows);
+        const IO *pz = static_cast<const IO *>(p.z) + token * p.z_stride + (int64_t)head * DIM + e;
+#pragma unroll
+        for (int i = 0; i < kGatedRows; ++i) {
+            if (i * PER < left) zr[i] = raw8(pz);
+            pz += p.z_step;
+            head += p.z_turn;
+            if (head >= p.z_rows) {
+                head -= p.z_rows;
+                pz += p.z_stride - (int64_t)p.z_rows * DIM;
+            }
         }
+    }
 #pragma unroll
     for (int i = 0; i < kGatedRows; ++i) {
         const bool live = i * PER < left;
@@ -250,15 +269,19 @@ int launch_add(NormParams &p, int out, bool vec, cudaStream_t st) {
 }
 
 template <typename IO, typename OUT>
-int launch_gated(const NormParams &p, cudaStream_t st) {
-    const int64_t per = (int64_t)256 / (p.dim / 8) * kGatedRows;
-    const dim3 grid((unsigned)((p.rows + per - 1) / per));
+int launch_gated(NormParams &p, cudaStream_t st) {
+    const int per = 256 / (p.dim / 8);
+    if (p.z_rows > 0) {
+        p.z_turn = per % p.z_rows;
+        p.z_step = per / p.z_rows * p.z_stride + (int64_t)p.z_turn * p.dim;
+    }
+    const dim3 grid((unsigned)((p.rows + per * kGatedRows - 1) / (per * kGatedRows)));
     return p.dim == 128 ? launch_serialised(gated_rms_norm_kernel<IO, OUT, 128>, grid, 256, 0, st, p)
                         : launch_serialised(gated_rms_norm_kernel<IO, OUT, 64>, grid, 256, 0, st, p);
 }
 
 template <typename IO>
-int launch_gated(const NormParams &p, int out, cudaStream_t st) {
+int launch_gated(NormParams &p, int out, cudaStream_t st) {
     switch (out) {
         case GDN_OUT_BF16: return launch_gated<IO, __nv_bfloat16>(p, st);
         case GDN_OUT_F32: return launch_gated<IO, float>(p, st);
@@ -286,26 +309,32 @@ extern "C" int add_rms_norm_fwd(const void *x, const void *residual, const void 
         return KKT_ERR_ALIGN;
     if (rows == 0) return KKT_OK;
     NormParams p;
+    p.z_rows = 0; p.z_stride = 0; p.z_turn = 0; p.z_step = 0;
     p.x = x; p.r = residual; p.z = nullptr; p.w = weight; p.y = y; p.r_out = residual_out; p.scales = scales;
-    p.rows = rows; p.dim = dim; p.group = group; p.groups = (dim + 127) / 128; p.inv_dim = 1.f / (float)dim; p.row_warps = 1; p.eps = eps;
+    p.rows = rows; p.dim = dim; p.group = group; p.groups = (dim + 127) / 128; p.inv_dim = 1.f / (float)dim;
+    p.row_warps = 1; p.eps = eps;
     const bool vec = dim % 8 == 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return io_dtype == KKT_IO_BF16 ? launch_add<__nv_bfloat16>(p, out_dtype, vec, st)
                                    : launch_add<float>(p, out_dtype, vec, st);
 }
 
-extern "C" int gated_rms_norm_fwd(const void *x, const void *z, const void *weight, int64_t rows, int dim, float eps,
-                                  int io_dtype, int out_dtype, void *y, float *scales, struct CUstream_st *stream) {
+extern "C" int gated_rms_norm_fwd(const void *x, const void *z, int z_rows, int64_t z_stride, const void *weight,
+                                  int64_t rows, int dim, float eps, int io_dtype, int out_dtype, void *y, float *scales, struct CUstream_st *stream) {
     using namespace kkt;
     if (rows < 0 || dim < 1 || !types_ok(io_dtype, out_dtype)) return KKT_ERR_ARG;
     if (dim != 64 && dim != 128) return KKT_ERR_UNSUPPORTED;
     if (rows / 64 > 0x7ffffff0LL) return KKT_ERR_ARG;
+    constexpr int64_t kFar = (int64_t)1 << 31;
+    if (z_rows < 0 || (z_rows > 0 && (rows % z_rows != 0 || z_stride < (int64_t)z_rows * dim || z_stride > kFar || rows > kFar)))
+        return KKT_ERR_ARG;
     if (!weight || (rows > 0 && (!x || !z || !y || (out_dtype == GDN_OUT_E4M3 && !scales)))) return KKT_ERR_ARG;
     if (!aligned_ptr(x, 16) || !aligned_ptr(z, 16) || !aligned_ptr(weight, 16) || !aligned_ptr(y, 16) ||
-        !aligned_ptr(scales, 4))
+        !aligned_ptr(scales, 4) || (z_rows > 0 && z_stride * (io_dtype == KKT_IO_BF16 ? 2 : 4) % 16 != 0))
         return KKT_ERR_ALIGN;
     if (rows == 0) return KKT_OK;
     NormParams p;
+    p.z_rows = z_rows; p.z_stride = z_stride; p.z_turn = 0; p.z_step = 0;
     p.x = x; p.r = nullptr; p.z = z; p.w = weight; p.y = y; p.r_out = nullptr; p.scales = scales;
     p.rows = rows; p.dim = dim; p.group = 0; p.groups = 1; p.inv_dim = 1.f / (float)dim; p.row_warps = 1; p.eps = eps;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -43,6 +43,7 @@ struct PrepParams {
     void *conv_state, *q, *k, *v;
     float *g, *beta;
     int N, T, Hk, Hv, D, taps, expand, run, num_slots, slabs, gate_slabs, wide_weights;
+    int x_stride, a_stride, b_stride;  // values from a token to the next
     int64_t ntok;
     float eps;
     int *status;
@@ -92,20 +93,26 @@ __device__ __forceinline__ bool run_of(const PrepParams &p, int id, Run &r) {
 }
 
 // beta = sigmoid(b) and g = -e^{A_log} softplus(a + dt_bias) of `count` (token, head) pairs from token t0
-// on, every p.gate_slabs-th group of 32 of them from `part` on.
+// on, every p.gate_slabs-th group of 32 of them from `part` on.  The step from one to the next is a number
+// of tokens and of heads.
 template <typename IO>
 __device__ __forceinline__ void gates(const PrepParams &p, int t0, int count, int part, int lane) {
     const int64_t first = (int64_t)t0 * p.Hv;
-    const int stride = 32 * p.gate_slabs, turn = stride % p.Hv;
+    const int stride = 32 * p.gate_slabs, turn = stride % p.Hv, tokens = stride / p.Hv;
     int h = (part * 32 + lane) % p.Hv;
+    int64_t t = t0 + (part * 32 + lane) / p.Hv;
     for (int i = part * 32 + lane; i < count; i += stride) {
-        const float bb = to_f32(static_cast<const IO *>(p.b)[first + i]);
-        const float u = to_f32(static_cast<const IO *>(p.a)[first + i]) + p.dt_bias[h];
+        const float bb = to_f32(static_cast<const IO *>(p.b)[t * p.b_stride + h]);
+        const float u = to_f32(static_cast<const IO *>(p.a)[t * p.a_stride + h]) + p.dt_bias[h];
         p.beta[first + i] = 1.f / (1.f + expf(-bb));
         // softplus(u) = max(u, 0) + log(1 + e^-|u|); a NaN stays one
         p.g[first + i] = -expf(p.A_log[h]) * ((u > 0.f ? u : u < 0.f ? 0.f : u) + log1pf(expf(-fabsf(u))));
         h += turn;
-        if (h >= p.Hv) h -= p.Hv;
+        t += tokens;
+        if (h >= p.Hv) {
+            h -= p.Hv;
+            ++t;
+        }
     }
 }
 
@@ -226,23 +233,24 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
     const bool live = ch < p.D;  // the last slab may be short
     const int chc = live ? ch : 0;
     const int keep = p.taps - 1;
-    const int64_t D = p.D;
-    const IO *x = static_cast<const IO *>(p.x) + r.t0 * D + chc;  // the run's first row
+    const int64_t D = p.D, X = p.x_stride;
+    const IO *x = static_cast<const IO *>(p.x) + r.t0 * X + chc;  // the run's first row
 
     // a lane's 8 channels of a row have a place of their own, read back by the lane that copied them, so
     // that a wait for its own copies is all the ordering there is
     uint8_t *ring = smem + ((threadIdx.x >> 5) * kPrepStages * kPrepBatch * 32 + lane) * (8 * sizeof(IO));
     constexpr int kRowBytes = 32 * 8 * sizeof(IO);
     // the run's rows [from, from + kPrepBatch) into a stage
+    const IO *src = x;
     auto fetch = [&](int from, int stage) {
         uint8_t *d = ring + stage * (kPrepBatch * kRowBytes);
-        const IO *src = x + from * D;
 #pragma unroll
         for (int i = 0; i < kPrepBatch; ++i)
             if (from + i < r.count) {
-                copy16_async(d + i * kRowBytes, src + i * D);
-                if constexpr (sizeof(IO) == 4) copy16_async(d + i * kRowBytes + 16, src + i * D + 4);
+                copy16_async(d + i * kRowBytes, src + i * X);
+                if constexpr (sizeof(IO) == 4) copy16_async(d + i * kRowBytes + 16, src + i * X + 4);
             }
+        src += kPrepBatch * X;
         copy_commit();
     };
 #pragma unroll
@@ -259,7 +267,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
     if (r.t0 > r.a) {
 #pragma unroll
         for (int j = 0; j < 3; ++j)
-            if (3 - j <= keep) widen8(raw8(x - (3 - j) * D), win[j]);
+            if (3 - j <= keep) widen8(raw8(x - (3 - j) * X), win[j]);
     } else if (r.slot >= 0) {
         IO *state = static_cast<IO *>(p.conv_state) + (int64_t)r.slot * keep * D + chc;
 #pragma unroll
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
             const int len = r.b - r.a;
             for (int i = 0; i < keep; ++i) {
                 const int from = len + i;
-                store_raw8(state + i * D, from < keep ? raw8(state + from * D) : raw8(x + (from - keep) * D));
+                store_raw8(state + i * D, from < keep ? raw8(state + from * D) : raw8(x + (from - keep) * X));
             }
         }
     }
@@ -336,18 +344,18 @@ __global__ void __launch_bounds__(kPrepWarps * 32, sizeof(IO) == 2 ? (R == 1 ? 1
     const bool live = ch < p.D;
     const int chc = live ? ch : 0;
     const int keep = p.taps - 1;
-    const int64_t D = p.D;
-    const IO *x = static_cast<const IO *>(p.x) + r.t0 * D + chc;
+    const int64_t D = p.D, X = p.x_stride;
+    const IO *x = static_cast<const IO *>(p.x) + r.t0 * X + chc;
     Raw8<IO> row[3 + R] = {};  // the three inputs before the run, oldest first, and the run's
 #pragma unroll
     for (int i = 0; i < R; ++i)
-        if (i < r.count) row[3 + i] = raw8(x + i * D);
+        if (i < r.count) row[3 + i] = raw8(x + i * X);
     float2 w[4][4], bias[4];
     load_weights<IO>(p, chc, w, bias);
     if (r.t0 > r.a) {
 #pragma unroll
         for (int j = 0; j < 3; ++j)
-            if (3 - j <= keep) row[j] = raw8(x - (3 - j) * D);
+            if (3 - j <= keep) row[j] = raw8(x - (3 - j) * X);
     } else if (r.slot >= 0) {
         IO *state = static_cast<IO *>(p.conv_state) + (int64_t)r.slot * keep * D + chc;
 #pragma unroll
@@ -363,7 +371,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, sizeof(IO) == 2 ? (R == 1 ? 1
                     const int from = j + len;  // the row in its place, counted as `row` counts
                     Raw8<IO> v;
                     if (len > R) {
-                        v = raw8(x + (from - 3) * D);
+                        v = raw8(x + (from - 3) * X);
                     } else {
                         v = row[j + 1];
 #pragma unroll
@@ -417,8 +425,8 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
     if (!p.cu && p.T == 1) return launch_short<IO, 1>(p, dh, dim3((unsigned)p.N, blocks), st);
     // Tokens of a run.  A longer one reads fewer inputs before its first token and sets up less often; a
     // shorter one gives more warps.  The time goes as (tokens + 8) x waves of 16 warps an SM, whole ones
-    // while they are few: so the run with the least of that, sequences taken to be of one length.  Runs of 6, 18, 30 and 48 tokens take, in
-    // us: 207, 150, 133, 127 (27.9k tokens of 6144 channels; 48 taken), 64, 49, 45, 46 (8192 of them; 48),
+    // while they are few: so the run with the least of that, sequences taken to be of one length.  Runs
+    // of 6, 18, 30 and 48 tokens take, in us: 207, 150, 133, 127 (27.9k tokens of 6144 channels; 48 taken), 64, 49, 45, 46 (8192 of them; 48),
     // 14.1, 12.1, 14.6, 19.8 (1000 of 8192 channels; 18), 5.7, 8.0, 9.3, 12.3 (1.3k of 2048; 6).
     auto ids = [&] {
         return p.cu ? p.ntok / p.run + p.N : (int64_t)p.N * (((int64_t)p.T + p.run - 1) / p.run);
@@ -450,9 +458,9 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
 }  // namespace
 }  // namespace kkt
 
-extern "C" int gdn_prep_fwd(const void *x, const void *weight, const void *bias, const void *a, const void *b,
-                            const float *A_log, const float *dt_bias, const int32_t *cu_seqlens, int N, int T, int Hk,
-                            int Hv, int dk, int dv, int taps, float eps, int expand, int io_dtype, void *conv_state,
+extern "C" int gdn_prep_fwd(const void *x, int64_t x_stride, const void *weight, const void *bias, const void *a,
+                            int64_t a_stride, const void *b, int64_t b_stride, const float *A_log,
+                            const float *dt_bias, const int32_t *cu_seqlens, int N, int T, int Hk, int Hv, int dk, int dv, int taps, float eps, int expand, int io_dtype, void *conv_state,
                             int num_slots, const int32_t *slots, void *q, void *k, void *v, float *g, float *beta,
                             struct CUstream_st *stream) {
     using namespace kkt;
@@ -463,6 +471,8 @@ extern "C" int gdn_prep_fwd(const void *x, const void *weight, const void *bias,
     const int64_t D = ((int64_t)2 * Hk + Hv) * dk;
     if (ntok > 0x7fffff00LL || D > (int64_t)kSlab * 65535) return KKT_ERR_ARG;  // room for a batch past the end
     if (!weight || !A_log || !dt_bias) return KKT_ERR_ARG;
+    if (x_stride < D || a_stride < Hv || b_stride < Hv) return KKT_ERR_ARG;
+    if (x_stride > 0x7fffffffLL || a_stride > 0x7fffffffLL || b_stride > 0x7fffffffLL) return KKT_ERR_ARG;
     if (ntok > 0 && (!x || !a || !b || !q || !k || !v || !g || !beta)) return KKT_ERR_ARG;
     if (num_slots > 0 && !conv_state) return KKT_ERR_ARG;
     if (!slots && N > num_slots) return KKT_ERR_ARG;
@@ -470,7 +480,7 @@ extern "C" int gdn_prep_fwd(const void *x, const void *weight, const void *bias,
     if (!aligned_ptr(x, 16) || !aligned_ptr(weight, es) || !aligned_ptr(bias, es) || !aligned_ptr(a, es) ||
         !aligned_ptr(b, es) || !aligned_ptr(A_log, 4) || !aligned_ptr(dt_bias, 4) || !aligned_ptr(cu_seqlens, 4) ||
         !aligned_ptr(slots, 4) || !aligned_ptr(conv_state, 16) || !aligned_ptr(q, 16) || !aligned_ptr(k, 16) ||
-        !aligned_ptr(v, 16) || !aligned_ptr(g, 4) || !aligned_ptr(beta, 4))
+        !aligned_ptr(v, 16) || !aligned_ptr(g, 4) || !aligned_ptr(beta, 4) || x_stride * es % 16 != 0)
         return KKT_ERR_ALIGN;
     if (ntok == 0) return KKT_OK;
     PrepParams p;
@@ -479,6 +489,7 @@ extern "C" int gdn_prep_fwd(const void *x, const void *weight, const void *bias,
     p.conv_state = conv_state; p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta;
     p.N = N; p.T = T; p.Hk = Hk; p.Hv = Hv; p.D = (int)D; p.taps = taps; p.expand = expand != 0;
     p.num_slots = num_slots; p.ntok = ntok; p.eps = eps;
+    p.x_stride = (int)x_stride; p.a_stride = (int)a_stride; p.b_stride = (int)b_stride;
     const int rc = status_ptr(&p.status);
     if (rc != KKT_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

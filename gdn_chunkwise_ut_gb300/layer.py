@@ -67,7 +67,9 @@ def gdn_prep_fwd(x: torch.Tensor, weight: torch.Tensor, a: torch.Tensor, b: torc
     slot n; negative: zeros, not written), and is updated in place to the sequence's last ones.
     q, k are [B, T, Hk, dk], or with ``expand`` [B, T, Hv, dk], each key head repeated for the value
     heads that use it, as ``chunk_gated_delta_rule`` takes them.  v [B, T, Hv, dv]; g, beta fp32
-    [B, T, Hv].  dk = dv = 64 or 128.  ``cu_seqlens`` as in ``gdn_recurrent_fwd``.
+    [B, T, Hv].  dk = dv = 64 or 128.  ``cu_seqlens`` as in ``gdn_recurrent_fwd``.  x, a and b may be
+    slices of one tensor [B, T, W], as one product for all projections gives them (x at a multiple of
+    16 bytes).
     """
     if stream is not None:
         with torch.cuda.stream(stream):
@@ -103,7 +105,8 @@ def gated_rms_norm_fwd(x: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *
 
     x (the delta rule's o) and ``z`` [..., d], ``weight`` [d], bf16 or fp32, all one type; d is 64 or
     128.  ``out_dtype`` as in ``add_rms_norm_fwd``; in 8 bits ``scales`` [...] fp32 holds one for each
-    head of each token.
+    head of each token.  z may be a view of a slice, each token's heads contiguous (at multiples of 16
+    bytes) and equal steps from token to token.
     """
     if stream is not None:
         with torch.cuda.stream(stream):

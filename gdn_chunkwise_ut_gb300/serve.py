@@ -6,7 +6,7 @@
 projection, ``gdn_prep_fwd``, the chunked delta rule and the gated norm, and leaves its states in its
 slot; a decode step takes the same way with ``gdn_recurrent_fwd`` in the chunked rule's place, and is
 the same kernels at fixed addresses each time, so that it can be captured into a CUDA graph.  The
-projections are plain matrix products, with random weights.
+projections are one plain matrix product, whose parts the operators read in place; random weights.
 """
 from __future__ import annotations
 
@@ -33,9 +33,10 @@ class GdnLayer:
             return (scale * torch.randn(shape, generator=gen, device=device, dtype=torch.float32)).to(dtype)
 
         self.norm = 1.0 + randn(dim, scale=0.1)
-        self.qkv = randn(dim, D, scale=dim ** -0.5)
-        self.z = randn(dim, Hv * self.d, scale=dim ** -0.5)
-        self.a, self.b = randn(dim, Hv, scale=dim ** -0.5), randn(dim, Hv, scale=dim ** -0.5)
+        # one product for all projections, cut into the convolution's channels, the gates' inputs and z
+        # (padded so that z, and the next token's channels, begin on 16 bytes)
+        self.parts = [D, Hv, Hv, -2 * Hv % 8, Hv * self.d]
+        self.proj = randn(dim, sum(self.parts), scale=dim ** -0.5)
         self.conv = randn(D, self.taps, scale=0.5)
         self.A_log = torch.log(1.0 + 15.0 * torch.rand(Hv, generator=gen, device=device))
         self.dt_bias = randn(Hv, dtype=torch.float32) - 4.0
@@ -43,24 +44,24 @@ class GdnLayer:
         self.out = randn(Hv * self.d, dim, scale=(Hv * self.d) ** -0.5)
 
     def pool(self, num_slots: int) -> StatePool:
-        return StatePool(num_slots, 1, self.Hk, self.Hv, self.d, self.d, taps=self.taps, device=self.qkv.device)
+        return StatePool(num_slots, 1, self.Hk, self.Hv, self.d, self.d, taps=self.taps, device=self.proj.device)
 
     def _inputs(self, x, residual, pool, slots, cu_seqlens, expand):
         h, _, residual = add_rms_norm_fwd(x, self.norm, residual)
-        q, k, v, g, beta = gdn_prep_fwd(h @ self.qkv, self.conv, h @ self.a, h @ self.b, self.A_log, self.dt_bias,
-                                        pool.convs[0], Hk=self.Hk, Hv=self.Hv, dk=self.d, dv=self.d, slots=slots,
-                                        cu_seqlens=cu_seqlens, expand=expand)
-        return h, residual, q, k, v, g, beta
+        qkv, a, b, _, z = (h @ self.proj).split(self.parts, dim=-1)
+        q, k, v, g, beta = gdn_prep_fwd(qkv, self.conv, a, b, self.A_log, self.dt_bias, pool.convs[0], Hk=self.Hk,
+                                        Hv=self.Hv, dk=self.d, dv=self.d, slots=slots, cu_seqlens=cu_seqlens,
+                                        expand=expand)
+        return z.unflatten(-1, (self.Hv, self.d)), residual, q, k, v, g, beta
 
-    def _outputs(self, o, h):
-        z = (h @ self.z).view(o.shape)
+    def _outputs(self, o, z):
         y, _ = gated_rms_norm_fwd(o, z, self.out_norm)
-        return y.reshape(*h.shape[:-1], -1) @ self.out
+        return y.flatten(-2) @ self.out
 
     def prefill(self, x, residual, pool: StatePool, slots, cu_seqlens):
         """Packed prompts x, residual [1, T, dim]: returns (output, new residual); the slots take the
         prompts' states on from the ones that they hold."""
-        h, residual, q, k, v, g, beta = self._inputs(x, residual, pool, slots, cu_seqlens, True)
+        z, residual, q, k, v, g, beta = self._inputs(x, residual, pool, slots, cu_seqlens, True)
         n = slots.shape[0]
         first = torch.arange(n, dtype=torch.int32, device=x.device)
         state = torch.empty((n, self.Hv, self.d, self.d), dtype=torch.float32, device=x.device)
@@ -68,13 +69,13 @@ class GdnLayer:
         o, final = chunk_gated_delta_rule(q, k, v, g, beta, initial_state=state, output_final_state=True,
                                           cu_seqlens=cu_seqlens)
         gdn_state_copy(pool.states[0], slots, final, first)
-        return self._outputs(o, h), residual
+        return self._outputs(o, z), residual
 
     def decode(self, x, residual, pool: StatePool, slots):
         """One token a sequence, x, residual [N, 1, dim]: returns (output, new residual)."""
-        h, residual, q, k, v, g, beta = self._inputs(x, residual, pool, slots, None, False)
+        z, residual, q, k, v, g, beta = self._inputs(x, residual, pool, slots, None, False)
         o = gdn_recurrent_fwd(q, k, v, beta, pool.states[0], g=g, slots=slots)
-        return self._outputs(o, h), residual
+        return self._outputs(o, z), residual
 
 
 def main() -> None:

@@ -6,7 +6,8 @@
  *
  * Conventions: every pointer is a device pointer owned by the caller; the library allocates nothing;
  * calls are asynchronous on `stream` and never synchronise the host; tensors are row-major and
- * contiguous and 16-byte aligned, fp32 vectors and index arrays 4-byte aligned.  Invalid arguments
+ * contiguous (but for those with a stride of their own) and 16-byte aligned, fp32 vectors and index
+ * arrays 4-byte aligned.  Invalid arguments
  * return a nonzero kkt_status without launching.  What only the device can see (a malformed
  * cu_seqlens: KKT_ERR_SEQLENS; a slot at or past num_slots: KKT_ERR_INDEX) is recorded in the status
  * word that kkt_device_status() reads; the kernels leave the sequences concerned alone.
@@ -73,16 +74,19 @@ int gdn_recurrent_fwd(const void *q, const void *k, const void *v, const float *
  *
  *   x       [.., D]     io_dtype          weight [D, taps], bias [D] (or NULL)   io_dtype
  *   a, b    [.., Hv]    io_dtype          A_log, dt_bias [Hv]   fp32
+ *   x_stride, a_stride, b_stride          values from a token's to the next one's: D, Hv and Hv, or
+ *           more for slices of a larger tensor, as one product for all projections gives them (below
+ *           2^31; x_stride a multiple of 16 bytes; a, b and the weights aligned to their type only)
  *   conv_state [num_slots, taps - 1, D]   io_dtype, updated in place to the last taps - 1 inputs
  *   q, k    [.., Hk, dk] or, with expand, [.., Hv, dk] (each key head written once for every value
  *           head that uses it, as kkt_solve_fwd takes them);   v [.., Hv, dv];   io_dtype, outputs
  *   g, beta [.., Hv]    fp32, outputs
  *   dk = dv = 64 or 128;   taps 2, 3 or 4
  */
-int gdn_prep_fwd(const void *x, const void *weight, const void *bias, const void *a, const void *b,
-                 const float *A_log, const float *dt_bias, const int32_t *cu_seqlens, int N, int T, int Hk, int Hv,
-                 int dk, int dv, int taps, float eps, int expand, int io_dtype, void *conv_state, int num_slots,
-                 const int32_t *slots, void *q, void *k, void *v, float *g, float *beta, struct CUstream_st *stream);
+int gdn_prep_fwd(const void *x, int64_t x_stride, const void *weight, const void *bias, const void *a,
+                 int64_t a_stride, const void *b, int64_t b_stride, const float *A_log, const float *dt_bias,
+                 const int32_t *cu_seqlens, int N, int T, int Hk, int Hv, int dk, int dv, int taps, float eps,
+                 int expand, int io_dtype, void *conv_state, int num_slots, const int32_t *slots, void *q, void *k, void *v, float *g, float *beta, struct CUstream_st *stream);
 
 /*
  * add_rms_norm_fwd -- h = x + residual (h = x where residual is NULL), residual_out = h, and
@@ -100,10 +104,12 @@ int add_rms_norm_fwd(const void *x, const void *residual, const void *weight, in
 /*
  * gated_rms_norm_fwd -- y = x / sqrt(mean(x^2) + eps) * weight * silu(z) over rows of `dim` (one head
  * of one token: dim 64 or 128).  x, z [rows, dim], weight [dim]: io_dtype; y [rows, dim]: out_dtype;
- * with GDN_OUT_E4M3, scales [rows] fp32: one for each row, as in add_rms_norm_fwd.
+ * with GDN_OUT_E4M3, scales [rows] fp32: one for each row, as in add_rms_norm_fwd.  z_rows: 0, or z
+ * is a slice of a larger tensor, z_rows rows (a token's heads) behind one another and z_stride values
+ * from the first of them to the next token's (a multiple of 16 bytes, at most 2^31).
  */
-int gated_rms_norm_fwd(const void *x, const void *z, const void *weight, int64_t rows, int dim, float eps,
-                       int io_dtype, int out_dtype, void *y, float *scales, struct CUstream_st *stream);
+int gated_rms_norm_fwd(const void *x, const void *z, int z_rows, int64_t z_stride, const void *weight,
+                       int64_t rows, int dim, float eps, int io_dtype, int out_dtype, void *y, float *scales, struct CUstream_st *stream);
 
 /* Tensors of one gdn_state_copy call. */
 #define GDN_COPY_MAX_TENSORS 64
@@ -111,8 +117,9 @@ int gated_rms_norm_fwd(const void *x, const void *z, const void *weight, int64_t
 /*
  * gdn_state_copy -- copies pool slots: for every tensor i < ntensors and every m < nmoves,
  *   dst[i] slot dst_slots[m]  <-  src[i] slot src_slots[m],
- * or zeros where src_slots[m] is negative or src is NULL.  A negative dst_slots[m] is skipped.  Forking is a source named more than once; freeing is clearing.  A slot is slot_bytes[i]
- * consecutive bytes, and slots are dst_stride[i] (src_stride[i]) bytes apart.
+ * or zeros where src_slots[m] is negative or src is NULL.  A negative dst_slots[m] is skipped.
+ * Forking is a source named more than once; freeing is clearing.  A slot is slot_bytes[i] consecutive
+ * bytes, and slots are dst_stride[i] (src_stride[i]) bytes apart.
  *   dst, src, slot_bytes, dst_stride, src_stride   HOST arrays of ntensors (at most
  *                         GDN_COPY_MAX_TENSORS) device pointers and byte counts
  *   dst_slots, src_slots  device int32[nmoves], below dst_num_slots / src_num_slots

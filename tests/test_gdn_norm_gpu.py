@@ -183,3 +183,30 @@ def test_misaligned_inputs_are_refused():
         add_rms_norm_fwd(raw[1:].view(2, 128), w)
     with pytest.raises(_lib.KktError, match="misaligned"):
         gated_rms_norm_fwd(raw[1:].view(2, 128), randn(2, 128), w)
+
+
+@pytest.mark.parametrize("out", [None, FP8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads", [1, 3, 16, 21, 100])
+@pytest.mark.parametrize("shape", [(1, 1), (5, 1), (2, 37), (1, 300)])
+def test_gated_rms_norm_z_from_a_slice(shape, heads, d, out):
+    """z as a part of a larger tensor, or every second head of it, gives the bits of its copy."""
+    x, whole, w = randn(*shape, heads, d, seed=20), randn(*shape, 8 + 2 * heads * d + 16, seed=21), randn(d, seed=22)
+    for z in (whole[..., 8:8 + heads * d].unflatten(-1, (heads, d)),
+              whole[..., :2 * heads * d].contiguous().unflatten(-1, (2 * heads, d))[..., ::2, :]):
+        want = gated_rms_norm_fwd(x, z.contiguous(), w, out_dtype=out)
+        got = gated_rms_norm_fwd(x, z, w, out_dtype=out)
+        assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8))
+        assert out is None or torch.equal(got[1], want[1])
+
+
+def test_gated_rms_norm_slices_that_are_refused():
+    x, w = randn(2, 3, 4, 128), randn(128)
+    wide = randn(2, 5, 4 * 128 + 12)
+    for bad in (wide[:, :3, :512].unflatten(-1, (4, 128)), randn(2, 3, 4, 256)[..., ::2], x[:, :1].expand(2, 3, 4, 128),
+                x[..., :1].expand(2, 3, 4, 128), randn(2, 3, 128, 4).transpose(2, 3), randn(3, 2, 4, 128).transpose(0, 1)):
+        with pytest.raises(ValueError, match="slice|rows must be contiguous"):
+            gated_rms_norm_fwd(x, bad, w)
+    with pytest.raises(_lib.KktError) as e:
+        gated_rms_norm_fwd(x, wide[:, :3].contiguous()[..., :512].unflatten(-1, (4, 128)), w)
+    assert e.value.status == _lib.KKT_ERR_ALIGN

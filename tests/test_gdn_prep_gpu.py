@@ -228,3 +228,43 @@ def test_misaligned_inputs_are_refused():
     raw = torch.zeros(t["x"].numel() + 1, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(_lib.KktError, match="misaligned"):
         gdn_prep_fwd(**dict(t, x=raw[1:].view(t["x"].shape)))
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape,cu", [((3, 1), None), ((1, 1), None), ((2, 3), None), ((2, 50), None),
+                                      ((1, 40), [0, 1, 1, 30, 40]), ((1, 9), [0, 2, 6, 9])])
+@pytest.mark.parametrize("Hv,d", [(2, 128), (34, 64)])
+def test_slices_of_one_projection(io, shape, cu, Hv, d):
+    """x, a and b as parts of one tensor give the bits of their copies."""
+    t = make(shape, 2, Hv, d, 8, io=io, seed=70)
+    D = t["x"].shape[-1]
+    whole = torch.full((*shape, 16 + D + 2 * Hv + 5 + -(2 * Hv + 5) % 8), float("nan"), device=DEV, dtype=io)
+    whole[..., 16:16 + D], whole[..., 16 + D + 3:16 + D + 3 + Hv] = t["x"], t["a"]
+    whole[..., 16 + D + 3 + Hv:16 + D + 3 + 2 * Hv] = t["b"]
+    cut = dict(t, conv_state=t["conv_state"].clone(), x=whole[..., 16:16 + D], a=whole[..., 16 + D + 3:16 + D + 3 + Hv],
+               b=whole[..., 16 + D + 3 + Hv:16 + D + 3 + 2 * Hv])
+    want = run_and_check(t, cu=cu)
+    out = gdn_prep_fwd(**cut, cu_seqlens=i32(cu))
+    torch.cuda.synchronize()
+    assert device_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(out, want)) and torch.equal(cut["conv_state"], t["conv_state"])
+
+
+def test_slices_that_are_refused():
+    t = make((2, 3), 2, 4, 64, 4)
+    D = t["x"].shape[-1]
+    wide = torch.zeros((2, 5, D + 12), dtype=torch.bfloat16, device=DEV)
+    for bad in (wide[:, :3, :D],                                     # a gap between the sequences
+                wide[:, :3, :1].expand(2, 3, D),                     # one value for all channels
+                t["x"][:, :1].expand(2, 3, D),                       # one token for all
+                wide.new_zeros((2, 3, 2 * D))[..., ::2],             # every second channel
+                wide.new_zeros((D, 3, 2)).permute(2, 1, 0)):
+        with pytest.raises(ValueError, match="slice"):
+            gdn_prep_fwd(**dict(t, x=bad))
+    with pytest.raises(ValueError, match="slice"):
+        gdn_prep_fwd(**dict(t, a=t["a"][:, :1].expand(2, 3, 4)))
+    for bad in (wide[:, :3].contiguous()[..., :D],                   # the next token's channels off 16 bytes
+                wide.new_zeros((2, 3, D + 8))[..., 4:4 + D]):        # the first one's
+        with pytest.raises(_lib.KktError) as e:
+            gdn_prep_fwd(**dict(t, x=bad))
+        assert e.value.status == _lib.KKT_ERR_ALIGN

@@ -66,18 +66,19 @@ def test_prep_argument_errors(lib):
     def call(**kw):
         a = dict(x=0x1000, w=0x2000, bias=None, a=0x3000, b=0x4000, A=0x5000, dt=0x6000, cu=None, N=2, T=1, Hk=2, Hv=4,
                  dk=128, dv=128, taps=4, expand=0, io=0, state=0x7000, P=8, slots=0x8000, q=0x9000, k=0xa000, v=0xb000,
-                 g=0xc000, beta=0xd000)
+                 g=0xc000, beta=0xd000, xs=1024, as_=4, bs=4)
         a.update(kw)
-        return lib.gdn_prep_fwd(a["x"], a["w"], a["bias"], a["a"], a["b"], a["A"], a["dt"], a["cu"], a["N"], a["T"],
-                                a["Hk"], a["Hv"], a["dk"], a["dv"], a["taps"], 1e-6, a["expand"], a["io"], a["state"],
+        return lib.gdn_prep_fwd(a["x"], a["xs"], a["w"], a["bias"], a["a"], a["as_"], a["b"], a["bs"], a["A"],
+                                a["dt"], a["cu"], a["N"], a["T"], a["Hk"], a["Hv"], a["dk"], a["dv"], a["taps"], 1e-6, a["expand"], a["io"], a["state"],
                                 a["P"], a["slots"], a["q"], a["k"], a["v"], a["g"], a["beta"], None)
     for bad in (dict(x=None), dict(w=None), dict(a=None), dict(A=None), dict(dt=None), dict(q=None), dict(beta=None),
-                dict(state=None), dict(N=0), dict(T=-1), dict(Hk=3), dict(io=5), dict(slots=None, N=9), dict(P=-2)):
+                dict(state=None), dict(N=0), dict(T=-1), dict(Hk=3), dict(io=5), dict(slots=None, N=9), dict(P=-2),
+                dict(xs=1016), dict(xs=0), dict(xs=1 << 40), dict(as_=3), dict(bs=-4), dict(bs=1 << 40)):
         assert call(**bad) == _lib.KKT_ERR_ARG, bad
     for bad in (dict(dk=96, dv=96), dict(dv=64), dict(taps=1), dict(taps=5)):
         assert call(**bad) == _lib.KKT_ERR_UNSUPPORTED, bad
     for bad in (dict(x=0x1008), dict(state=0x7004), dict(q=0x9008), dict(w=0x2001), dict(a=0x3001), dict(g=0xc002),
-                dict(slots=0x8002)):
+                dict(slots=0x8002), dict(xs=1028)):
         assert call(**bad) == _lib.KKT_ERR_ALIGN, bad
     assert call(T=0, x=None, a=None, b=None, q=None, k=None, v=None, g=None, beta=None) == _lib.KKT_OK
 
@@ -97,14 +98,15 @@ def test_norm_argument_errors(lib):
     assert add(rows=0, x=None, y=None) == _lib.KKT_OK
 
     def gated(**kw):
-        a = dict(x=0x1000, z=0x2000, w=0x3000, rows=2, dim=128, io=0, out=0, y=0x4000, s=None)
+        a = dict(x=0x1000, z=0x2000, w=0x3000, rows=2, dim=128, io=0, out=0, y=0x4000, s=None, zr=0, zs=0)
         a.update(kw)
-        return lib.gated_rms_norm_fwd(a["x"], a["z"], a["w"], a["rows"], a["dim"], 1e-6, a["io"], a["out"], a["y"],
-                                      a["s"], None)
+        return lib.gated_rms_norm_fwd(a["x"], a["z"], a["zr"], a["zs"], a["w"], a["rows"], a["dim"], 1e-6,
+                                      a["io"], a["out"], a["y"], a["s"], None)
     for bad in (dict(x=None), dict(z=None), dict(w=None), dict(y=None), dict(io=2), dict(out=-1), dict(out=2),
-                dict(rows=1 << 62)):
+                dict(rows=1 << 62), dict(zr=-1, zs=128), dict(zr=2, zs=255), dict(zr=2, zs=1 << 40), dict(zr=3, zs=512)):
         assert gated(**bad) == _lib.KKT_ERR_ARG, bad
     assert gated(dim=96) == _lib.KKT_ERR_UNSUPPORTED
+    assert gated(zr=2, zs=260) == _lib.KKT_ERR_ALIGN
     assert gated(z=0x2004) == _lib.KKT_ERR_ALIGN and gated(out=2, s=0x5001) == _lib.KKT_ERR_ALIGN
     assert gated(rows=0, x=None, z=None, y=None) == _lib.KKT_OK
 
