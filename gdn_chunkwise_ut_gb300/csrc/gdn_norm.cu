@@ -6,9 +6,9 @@
 // a value.  Both read every input once and write every output once, a row staying in registers between
 // the sum of squares and its use, and are bound by HBM: with the residual, 32768 rows of 4096 take
 // 154.6 us (104% of the copy rate), of 2048 80.0 us (100%), 8 bits out 145 us (97%); the gated one over
-// 32768 x 16 heads 60 us in bf16 (100%) and 55.4 us in 8 bits (91%), where instructions begin to count:
-// pairs of values share them (without, 71.5 us); the same holds without the residual in 8 bits (32768 x
-// 4096: 91 us where the bytes take 61).  Rows whose width is no multiple of 8 are loaded value
+// 32768 x 16 heads 58.6 us in bf16 (103%) and 50.3 us in 8 bits (100%), where instructions begin to count,
+// so that pairs of values share them; they bind without the residual in 8 bits (32768 x 4096: 91 us where
+// the bytes take 61).  Rows whose width is no multiple of 8 are loaded value
 // by value and run at half that rate (8467 rows of 7353, 8 bits out: 117 us for 65 us' bytes).
 #include "gdn_layer.cuh"
 
@@ -161,9 +161,11 @@ __global__ void __launch_bounds__(kNormWarps * 32, NV * Unit<VEC>::P > 32 ? 1 : 
     }
 }
 
-// DIM / 8 lanes a row, kGatedRows rows to a thread, whose loads are in flight together (8-bit and bf16
-// output: two rows 54.5 and 64.6 us, four 55.4 and 59.9, eight 63.6 and 65.7).
-constexpr int kGatedRows = 4;
+// DIM / 8 lanes a row, kGatedRows rows to a thread, whose loads are in flight together.  Of 32768 x 16 heads
+// in 8 bits and in bf16, and of 64 x 32 heads in 8 bits, one row takes 55.5, 58.5 and 1.67 us, two 50.3,
+// 58.6 and 1.81, three 50.4, 59.2 and 2.31, four 51.1, 59.4 and 2.58, eight 60.6, 60.5 and 3.60; z in a
+// slice, two rows: 54.9, 59.0 and 2.06.
+constexpr int kGatedRows = 2;
 template <typename IO, typename OUT, int DIM>
 __global__ void __launch_bounds__(256) gated_rms_norm_kernel(const NormParams p) {
     constexpr int L = DIM / 8, PER = 256 / L;  // lanes of a row; rows of the block at a time
@@ -324,7 +326,7 @@ extern "C" int gated_rms_norm_fwd(const void *x, const void *z, int z_rows, int6
     using namespace kkt;
     if (rows < 0 || dim < 1 || !types_ok(io_dtype, out_dtype)) return KKT_ERR_ARG;
     if (dim != 64 && dim != 128) return KKT_ERR_UNSUPPORTED;
-    if (rows / 64 > 0x7ffffff0LL) return KKT_ERR_ARG;
+    if (rows / (16 * kGatedRows) > 0x7ffffff0LL) return KKT_ERR_ARG;
     constexpr int64_t kFar = (int64_t)1 << 31;
     if (z_rows < 0 || (z_rows > 0 && (rows % z_rows != 0 || z_stride < (int64_t)z_rows * dim || z_stride > kFar || rows > kFar)))
         return KKT_ERR_ARG;
