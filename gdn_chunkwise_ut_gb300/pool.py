@@ -59,13 +59,16 @@ class SlotTable:
             self._live.remove(s)
             heapq.heappush(self._free, s)
 
-    def compact(self) -> dict:
-        """Moves the live slots into the lowest ones: returns {old: new} for those that move.  The moves
-        are from slots at or past the number of live ones into free slots below it, so that no move
-        writes what another one reads."""
+    def compaction(self) -> dict:
+        """The moves {old: new} that bring the live slots into the lowest ones, from slots at or past the
+        number of live ones into free slots below it, so that no move writes what another one reads."""
         n = len(self._live)
         holes = [s for s in range(n) if s not in self._live]
-        moves = dict(zip(sorted(s for s in self._live if s >= n), holes))
+        return dict(zip(sorted(s for s in self._live if s >= n), holes))
+
+    def compact(self) -> dict:
+        """Moves the live slots into the lowest ones: returns {old: new} for those that move."""
+        n, moves = len(self._live), self.compaction()
         self._live = set(range(n))
         self._free = list(range(n, self.num_slots))
         return moves
@@ -82,6 +85,8 @@ class StatePool:
 
     def __init__(self, num_slots: int, layers: int, Hk: int, Hv: int, dk: int, dv: int, *, taps: int = 4,
                  state_dtype=torch.float32, dtype=torch.bfloat16, device="cuda"):
+        if layers < 1:
+            raise ValueError("layers must be positive")
         if 2 * layers > _lib.GDN_COPY_MAX_TENSORS:
             raise ValueError(f"at most {_lib.GDN_COPY_MAX_TENSORS // 2} layers in one pool")
         self.table = SlotTable(num_slots)
@@ -89,7 +94,7 @@ class StatePool:
         self.convs = [torch.zeros((num_slots, taps - 1, 2 * Hk * dk + Hv * dv), dtype=dtype, device=device)
                       for _ in range(layers)]
         self._all = self.states + self.convs
-        self._device = torch.device(device)
+        self._device = self.states[0].device
 
     def index(self, slots, *, stream=None) -> torch.Tensor:
         """The slots as the int32 tensor that the operators take, for use on ``stream``."""
@@ -99,18 +104,29 @@ class StatePool:
     def alloc(self, n: int = 1, *, stream=None) -> list:
         """``n`` slots of zero states."""
         slots = self.table.alloc(n)
-        if slots:
-            gdn_state_copy(self._all, self.index(slots, stream=stream), stream=stream)
+        self._copy(slots, None, slots, stream)
         return slots
 
     def fork(self, slot: int, n: int = 1, *, stream=None) -> list:
         """``n`` new slots, each with a copy of ``slot``'s states."""
         self.table.require([slot])
         slots = self.table.alloc(n)
-        if slots:
-            gdn_state_copy(self._all, self.index(slots, stream=stream), self._all,
-                           self.index([slot] * n, stream=stream), stream=stream)
+        self._copy(slots, [slot] * n, slots, stream)
         return slots
+
+    def _copy(self, dst, src, new, stream):
+        """dst[i] from src[i], or from zeros; the ``new`` slots are free again where that is refused."""
+        if not dst:
+            return
+        try:
+            index = self.index(dst, stream=stream)
+            if src is None:
+                gdn_state_copy(self._all, index, stream=stream)
+            else:
+                gdn_state_copy(self._all, index, self._all, self.index(src, stream=stream), stream=stream)
+        except BaseException:
+            self.table.free(new)
+            raise
 
     def free(self, slots) -> None:
         """Gives the slots back.  Their contents stay until they are handed out again."""
@@ -118,8 +134,6 @@ class StatePool:
 
     def compact(self, *, stream=None) -> dict:
         """Moves the live slots into the lowest ones: returns {old: new} for the slots that moved."""
-        moves = self.table.compact()
-        if moves:
-            gdn_state_copy(self._all, self.index(moves.values(), stream=stream), self._all,
-                           self.index(moves.keys(), stream=stream), stream=stream)
-        return moves
+        moves = self.table.compaction()
+        self._copy(list(moves.values()), list(moves), [], stream)
+        return self.table.compact()

@@ -49,3 +49,27 @@ def test_compact_moves_are_independent_and_keep_every_state():
         assert sorted(after) == list(range(len(held)))       # nothing lost, the lowest slots
         assert all(t.is_live(s) for s in after) and len(t) == len(held) and t.free_slots == n - len(held)
         assert t.alloc(t.free_slots) == list(range(len(held), n))
+
+
+def test_a_refused_copy_leaves_the_table_as_it_was(monkeypatch):
+    """The copies fail (as a launch error or a lack of memory would make them): no slot is lost or moved."""
+    import torch
+
+    from gdn_chunkwise_ut_gb300 import StatePool, pool
+    monkeypatch.setattr(pool, "gdn_state_copy", lambda *a, **k: None)
+    monkeypatch.setattr(StatePool, "index", lambda self, slots, *, stream=None: torch.tensor(list(slots)))
+    p = StatePool(6, 1, 1, 1, 64, 64, device="cpu")
+    p.alloc(4)
+    p.free([1])
+
+    def fail(*a, **k):
+        raise RuntimeError("refused")
+    monkeypatch.setattr(pool, "gdn_state_copy", fail)
+    for call in (lambda: p.alloc(2), lambda: p.fork(0, 2), p.compact):
+        with pytest.raises(RuntimeError, match="refused"):
+            call()
+        assert len(p.table) == 3 and p.table.free_slots == 3 and all(p.table.is_live(s) for s in (0, 2, 3))
+    monkeypatch.setattr(pool, "gdn_state_copy", lambda *a, **k: None)
+    assert p.compact() == {3: 1} and p.alloc(1) == [3]
+    with pytest.raises(ValueError):
+        StatePool(6, 0, 1, 1, 64, 64, device="cpu")
