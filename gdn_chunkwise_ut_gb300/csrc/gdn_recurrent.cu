@@ -10,12 +10,12 @@
 // The columns of S are independent.  A warp owns 16 of them: lane = 4 r + c holds columns 4c .. 4c+3
 // of the rows DK/8 r .. DK/8 (r + 1) - 1, so a row's 16 columns are one 64-byte segment, and the
 // reductions over the rows are in-register sums and three shuffle steps that halve what they carry.
-// No barrier: a block is four such warps.
+// No barrier: a block is a few such warps.
 //
 // What bounds it: one token a sequence reads and writes the states and little else, so HBM does.  256
-// sequences of 64 heads, fp32 states: 2.16 GB in 309 us, 105% of the copy rate; 64 x 32 heads 43.3 us
-// (93%); bf16 states 184 us (89%) and 26.8 us (76%), where the memory latency of a warp's whole state
-// in registers weighs more.  One sequence of 16 heads takes 2.8 us, launch and latency.  In longer runs
+// sequences of 64 heads, fp32 states: 2.16 GB in 310 us, 104% of the copy rate; 64 x 32 heads 43.6 us
+// (93%); bf16 states 176 us (93%) and 25.8 us (79%), where the memory latency of a warp's whole state
+// in registers weighs more.  One sequence of 16 heads takes 2.6 us, launch and latency.  In longer runs
 // the tokens of a sequence depend on one another: about 0.35 us a token (500 tokens of one sequence:
 // 177 us), or, with the SMs full, the issue slots (33 sequences of 1 to 8 tokens, 16 heads, bf16
 // states: 16.9 us where the bytes take 5.5).  So:
@@ -99,22 +99,32 @@ __device__ __forceinline__ void store_row(float *p, const float2 (&v)[2]) {
 }
 __device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float2 (&v)[4]) { store8(p, v); }
 
+// Warps of a block where every sequence has one token.  Small blocks leave no warp's place empty until its
+// neighbours end, which counts where the fewest fit (a bf16 state with dk 128: 163 registers, 12 warps an SM);
+// larger ones keep the parts of a row together in time.  Blocks of one, two and four warps: bf16 states,
+// 64 x 32 heads 25.8, 26.8 and 26.9 us, 256 x 64 176, 179 and 183; fp32 states 44.1, 43.6 and 43.5, 316, 310
+// and 309, one sequence of 16 heads 2.34, 2.59 and 2.84; dk = dv = 64, 64 x 32 heads, fp32 10.4, 9.3 and 10.1,
+// bf16 9.1, 8.5 and 8.5.
+template <typename ST, int DK>
+constexpr int kStepWarps = sizeof(ST) == 2 && DK == 128 ? 1 : 2;
+
 // One token for every sequence: nothing to keep between tokens, so the state stays in registers as it
 // was loaded and is widened in either pass over it.  That lets a lane have 16 bytes of a row for a bf16
 // state too (8 columns, 32 to a warp): as many bytes in flight as for an fp32 state.  Sums in the order
 // of the kernel below, so that decode steps give the bits of one longer call.
 template <typename IO, typename ST, int DK, int DV>
-__global__ void __launch_bounds__(kRecWarps * 32, sizeof(ST) == 4 ? 4 : 3) gdn_recurrent_step_kernel(const RecParams p) {
-    constexpr int R = DK / 8, C = 16 / sizeof(ST), E = C / 4;
+__global__ void __launch_bounds__(kStepWarps<ST, DK> * 32, (sizeof(ST) == 4 ? 16 : 12) / kStepWarps<ST, DK>)
+    gdn_recurrent_step_kernel(const RecParams p) {
+    constexpr int R = DK / 8, C = 16 / sizeof(ST), E = C / 4, W = kStepWarps<ST, DK>;
     constexpr int kParts = DV / (4 * C);  // warps of a (sequence, head)
     using Row = std::conditional_t<sizeof(ST) == 4, float4, uint4>;
     griddep_launch_dependents();
     griddep_wait();
     // a block has a part of one (sequence, head), or several of them whole
-    constexpr int kBlocks = kParts > kRecWarps ? kParts / kRecWarps : 1, kPairs = kParts < kRecWarps ? kRecWarps / kParts : 1;
+    constexpr int kBlocks = kParts > W ? kParts / W : 1, kPairs = kParts < W ? W / kParts : 1;
     const int warp = threadIdx.x >> 5;
     const int pair = (int)(blockIdx.x / kBlocks) * kPairs + warp / kParts;
-    const int part = (blockIdx.x % kBlocks) * kRecWarps + warp % kParts;
+    const int part = (blockIdx.x % kBlocks) * W + warp % kParts;
     if (pair >= p.N * p.Hv) return;
     const int n = pair / p.Hv, h = pair % p.Hv;
     const int lane = threadIdx.x & 31, r = lane >> 2, row0 = r * R;
@@ -324,14 +334,13 @@ __global__ void __launch_bounds__(kRecWarps * 32) gdn_recurrent_kernel(const Rec
 template <typename IO, typename ST, int DK, int DV>
 int launch(const RecParams &p, cudaStream_t st) {
     const int64_t pairs = (int64_t)p.N * p.Hv;
-    // One token a sequence: the kernel for it against the general one: 64 x 32 heads in bf16 states 26.8
-    // against 29.9 us, 256 x 64 184 against 202, fp32 states 43.3 and 309 in either, one sequence of 16
-    // heads 2.8 against 3.1.
-    if (!p.cu && p.T == 1) {
-        constexpr int kParts = DV * (int)sizeof(ST) / 64;
-        const dim3 grid((unsigned)((pairs * kParts + kRecWarps - 1) / kRecWarps));
-        return launch_serialised(gdn_recurrent_step_kernel<IO, ST, DK, DV>, grid, kRecWarps * 32, 0, st, p);
-    }
+    // One token a sequence: the kernel for it against the general one: 64 x 32 heads in bf16 states 25.8
+    // against 29.9 us, 256 x 64 176 against 202, fp32 states 43.6 and 310 in either, one sequence of 16 heads
+    // 2.6 against 3.1.
+    constexpr int kParts = DV * (int)sizeof(ST) / 64, W = kStepWarps<ST, DK>;
+    const int64_t blocks = (pairs * kParts + W - 1) / W;
+    if (!p.cu && p.T == 1 && blocks <= 0x7fffffffLL)
+        return launch_serialised(gdn_recurrent_step_kernel<IO, ST, DK, DV>, dim3((unsigned)blocks), W * 32, 0, st, p);
     const dim3 grid((unsigned)(pairs * (DV / 16 / kRecWarps)));
     return launch_serialised(gdn_recurrent_kernel<IO, ST, DK, DV>, grid, kRecWarps * 32, 0, st, p);
 }
