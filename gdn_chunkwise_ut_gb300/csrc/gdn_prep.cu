@@ -8,14 +8,15 @@
 // head's sum of squares is a shuffle over its 8 or 16 lanes.  The gates are slabs of their own, 16 heads each.
 //
 // What bounds it: by bytes HBM (the 27.9k packed tokens of 6144 channels of the bf16 prefill case
-// move 686 MB, 103 us at the copy rate; it takes 126.7 us, 81%), but the arithmetic keeps the issue slots
+// move 686 MB, 103 us at the copy rate; it takes 124.2 us, 83%), but the arithmetic keeps the issue slots
 // more than half busy, so the kernel is written against latency and instructions:
 //   - the inputs go through a ring of rows in shared memory by asynchronous copies, nine rows ahead,
 //     each lane reading back what it copied itself (no barrier), so that no registers wait on memory;
 //   - three tokens, the window's turn, are computed side by side, and pairs of channels share one
 //     fp32 instruction (128 us; one token after the other 140 us, with scalar arithmetic 192 us);
 //   - 8 channels a lane in 128 registers, 16 warps an SM (4 channels a lane: twice the warps, but more
-//     instructions a channel, 157 us); blocks of two warps, since a block's idle warps hold registers.
+//     instructions a channel, 157 us); blocks of one warp, whose registers are free for the next one when
+//     it ends (two warps 126.3 us).
 //
 // The convolution's state is read, and its successor written, by the warp that has the sequence's
 // first token, whichever run holds the last one: the same thread reads and writes each element, so
@@ -29,7 +30,9 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kPrepWarps = 2;
+constexpr int kPrepWarps = 1;   // of a block of the general kernel
+constexpr int kShortWarps = 2;  // of the one for short runs: one, two and four warps 10.4, 8.5 and 8.3 us for
+                                // 256 tokens of 8192 channels, 72.9, 51.7 and 52.3 for 2048
 constexpr int kPrepBatch = 3;   // tokens whose inputs are copied together: the window's turn
 constexpr int kPrepStages = 4;  // such copies in flight, with the one in use
 static_assert(kPrepBatch == 3, "the window's registers take turns with the tokens of a batch");
@@ -214,7 +217,7 @@ __device__ __forceinline__ void finish(const PrepParams &p, const HeadOut<IO> &h
 }
 
 template <typename IO, int DH>
-__global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const PrepParams p) {
+__global__ void __launch_bounds__(kPrepWarps * 32, 16) gdn_prep_kernel(const PrepParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     griddep_launch_dependents();
     griddep_wait();
@@ -316,12 +319,12 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 8) gdn_prep_kernel(const Prep
 // with many sequences, by HBM: of 8192 channels in bf16, a token for 64 sequences takes 3.2 us (the bytes
 // 1.3), for 256 8.5 us (5.1), for 2048 51 us (40), four for 256 13.4 us (8.9).
 template <typename IO, int DH, int R>
-__global__ void __launch_bounds__(kPrepWarps * 32, sizeof(IO) == 2 ? (R == 1 ? 14 : 10) : (R == 1 ? 10 : 7))
+__global__ void __launch_bounds__(kShortWarps * 32, sizeof(IO) == 2 ? (R == 1 ? 14 : 10) : (R == 1 ? 10 : 7))
     gdn_prep_short_kernel(const PrepParams p) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int slab = blockIdx.y * kPrepWarps + (threadIdx.x >> 5);
+    const int slab = blockIdx.y * kShortWarps + (threadIdx.x >> 5);
     if (slab >= p.slabs + p.gate_slabs) return;
     Run r;
     if constexpr (R == 1) {
@@ -409,8 +412,8 @@ int launch(const PrepParams &p, dim3 grid, cudaStream_t st) {
 
 template <typename IO, int R>
 int launch_short(const PrepParams &p, int dh, dim3 grid, cudaStream_t st) {
-    return dh == 128 ? launch_serialised(gdn_prep_short_kernel<IO, 128, R>, grid, kPrepWarps * 32, 0, st, p)
-                     : launch_serialised(gdn_prep_short_kernel<IO, 64, R>, grid, kPrepWarps * 32, 0, st, p);
+    return dh == 128 ? launch_serialised(gdn_prep_short_kernel<IO, 128, R>, grid, kShortWarps * 32, 0, st, p)
+                     : launch_serialised(gdn_prep_short_kernel<IO, 64, R>, grid, kShortWarps * 32, 0, st, p);
 }
 
 template <typename IO>
@@ -418,7 +421,8 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
     p.slabs = (p.D + kSlab - 1) / kSlab;
     p.gate_slabs = (p.Hv + 15) / 16;  // a token's 16 gates take about as long as its 256 channels
     p.wide_weights = aligned_ptr(p.weight, 16);
-    const unsigned blocks = (unsigned)((p.slabs + p.gate_slabs + kPrepWarps - 1) / kPrepWarps);
+    const int slabs = p.slabs + p.gate_slabs;
+    const unsigned blocks = (unsigned)((slabs + kShortWarps - 1) / kShortWarps);
     // Short runs against long ones, of 8192 channels: one token for 64 sequences 3.2 against 4.7 us, for 256
     // 8.5 against 20.8, for 2048 51 against 136; four tokens for 256 13.4 against 18.5, three for 2048 92
     // against 111; 256 packed sequences of one token 13.8 against 20.7.
@@ -451,7 +455,7 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
     }
     p.run = best;
     if (ids() > 0x7fffffffLL) return KKT_ERR_ARG;
-    const dim3 grid((unsigned)ids(), blocks);
+    const dim3 grid((unsigned)ids(), (unsigned)((slabs + kPrepWarps - 1) / kPrepWarps));
     return dh == 128 ? launch<IO, 128>(p, grid, st) : launch<IO, 64>(p, grid, st);
 }
 
@@ -469,7 +473,8 @@ extern "C" int gdn_prep_fwd(const void *x, int64_t x_stride, const void *weight,
     if (dk != dv || (dk != 64 && dk != 128) || taps < 2 || taps > 4) return KKT_ERR_UNSUPPORTED;
     const int64_t ntok = cu_seqlens ? (int64_t)T : (int64_t)N * T;
     const int64_t D = ((int64_t)2 * Hk + Hv) * dk;
-    if (ntok > 0x7fffff00LL || D > (int64_t)kSlab * 65535) return KKT_ERR_ARG;  // room for a batch past the end
+    // room for a batch past the end; the slabs are one axis of the grid
+    if (ntok > 0x7fffff00LL || (D + kSlab - 1) / kSlab + (Hv + 15) / 16 > 65535) return KKT_ERR_ARG;
     if (!weight || !A_log || !dt_bias) return KKT_ERR_ARG;
     if (x_stride < D || a_stride < Hv || b_stride < Hv) return KKT_ERR_ARG;
     if (x_stride > 0x7fffffffLL || a_stride > 0x7fffffffLL || b_stride > 0x7fffffffLL) return KKT_ERR_ARG;
