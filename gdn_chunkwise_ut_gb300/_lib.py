@@ -44,7 +44,6 @@ GDN_COPY_MAX_TENSORS = 64
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
-_i64 = ctypes.c_int64
 
 SIGNATURES = {
     "kkt_solve_fwd": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
@@ -55,9 +54,10 @@ SIGNATURES = {
     "gdn_chunk_state_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, ctypes.c_float, _vp,
                                  _vp, _vp]),
     "gdn_recurrent_fwd": (_i, [_vp] * 6 + [_i] * 6 + [ctypes.c_float, _i, _vp, _i, _i, _vp, _vp, _vp, _vp]),
-    "gdn_prep_fwd": (_i, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp] + [_i] * 7 + [ctypes.c_float, _i, _i, _vp, _i] + [_vp] * 7),
+    "gdn_prep_fwd": (_i, [_vp, _sz, _vp, _vp, _vp, _sz, _vp, _sz, _vp, _vp, _vp] + [_i] * 7 +
+                     [ctypes.c_float, _i, _i, _vp, _i] + [_vp] * 7),
     "add_rms_norm_fwd": (_i, [_vp, _vp, _vp, _sz, _i, ctypes.c_float, _i, _i, _i, _vp, _vp, _vp, _vp]),
-    "gated_rms_norm_fwd": (_i, [_vp, _vp, _i, _i64, _vp, _sz, _i, ctypes.c_float, _i, _i, _vp, _vp, _vp]),
+    "gated_rms_norm_fwd": (_i, [_vp, _vp, _i, _sz, _vp, _sz, _i, ctypes.c_float, _i, _i, _vp, _vp, _vp]),
     "gdn_state_copy": (_i, [_vp] * 5 + [_i, _vp, _vp, _i, _i, _i, _vp]),
     "kkt_host_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i, _i]),
     "kkt_solve_fwd_host": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _sz,
