@@ -322,13 +322,15 @@ extern "C" int add_rms_norm_fwd(const void *x, const void *residual, const void 
 }
 
 extern "C" int gated_rms_norm_fwd(const void *x, const void *z, int z_rows, int64_t z_stride, const void *weight,
-                                  int64_t rows, int dim, float eps, int io_dtype, int out_dtype, void *y, float *scales, struct CUstream_st *stream) {
+                                  int64_t rows, int dim, float eps, int io_dtype, int out_dtype, void *y,
+                                  float *scales, struct CUstream_st *stream) {
     using namespace kkt;
     if (rows < 0 || dim < 1 || !types_ok(io_dtype, out_dtype)) return KKT_ERR_ARG;
     if (dim != 64 && dim != 128) return KKT_ERR_UNSUPPORTED;
     if (rows / (16 * kGatedRows) > 0x7ffffff0LL) return KKT_ERR_ARG;
     constexpr int64_t kFar = (int64_t)1 << 31;
-    if (z_rows < 0 || (z_rows > 0 && (rows % z_rows != 0 || z_stride < (int64_t)z_rows * dim || z_stride > kFar || rows > kFar)))
+    if (z_rows < 0) return KKT_ERR_ARG;
+    if (z_rows > 0 && (rows % z_rows != 0 || z_stride < (int64_t)z_rows * dim || z_stride > kFar || rows > kFar))
         return KKT_ERR_ARG;
     if (!weight || (rows > 0 && (!x || !z || !y || (out_dtype == GDN_OUT_E4M3 && !scales)))) return KKT_ERR_ARG;
     if (!aligned_ptr(x, 16) || !aligned_ptr(z, 16) || !aligned_ptr(weight, 16) || !aligned_ptr(y, 16) ||

@@ -430,8 +430,9 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
     // Tokens of a run.  A longer one reads fewer inputs before its first token and sets up less often; a
     // shorter one gives more warps.  The time goes as (tokens + 8) x waves of 16 warps an SM, whole ones
     // while they are few: so the run with the least of that, sequences taken to be of one length.  Runs
-    // of 6, 18, 30 and 48 tokens take, in us: 207, 150, 133, 127 (27.9k tokens of 6144 channels; 48 taken), 64, 49, 45, 46 (8192 of them; 48),
-    // 14.1, 12.1, 14.6, 19.8 (1000 of 8192 channels; 18), 5.7, 8.0, 9.3, 12.3 (1.3k of 2048; 6).
+    // of 6, 18, 30 and 48 tokens take, in us: 191, 141, 128, 124 (27.9k tokens of 6144 channels; 48 taken),
+    // 61, 48, 45, 46 (8192 of them; 48), 13.9, 11.8, 14.6, 19.8 (1000 of 8192 channels; 18), 5.4, 7.2, 9.0,
+    // 12.1 (1.3k of 2048; 6).
     auto ids = [&] {
         return p.cu ? p.ntok / p.run + p.N : (int64_t)p.N * (((int64_t)p.T + p.run - 1) / p.run);
     };
@@ -464,8 +465,9 @@ int launch(PrepParams &p, int dh, cudaStream_t st) {
 
 extern "C" int gdn_prep_fwd(const void *x, int64_t x_stride, const void *weight, const void *bias, const void *a,
                             int64_t a_stride, const void *b, int64_t b_stride, const float *A_log,
-                            const float *dt_bias, const int32_t *cu_seqlens, int N, int T, int Hk, int Hv, int dk, int dv, int taps, float eps, int expand, int io_dtype, void *conv_state,
-                            int num_slots, const int32_t *slots, void *q, void *k, void *v, float *g, float *beta,
+                            const float *dt_bias, const int32_t *cu_seqlens, int N, int T, int Hk, int Hv, int dk,
+                            int dv, int taps, float eps, int expand, int io_dtype, void *conv_state, int num_slots,
+                            const int32_t *slots, void *q, void *k, void *v, float *g, float *beta,
                             struct CUstream_st *stream) {
     using namespace kkt;
     if (N < 1 || T < 0 || Hk < 1 || Hv < 1 || Hv > 65535 || Hv % Hk != 0 || num_slots < 0) return KKT_ERR_ARG;
